@@ -332,6 +332,129 @@ rmm_status rmm_qkv_heads(const void* Yq, const void* Yk, const void* Yv, int T, 
  * A[t, h*d + j] = O[h, t, j] for O [Hq, T, d] (batch 1), d == 128. */
 rmm_status rmm_heads_to_tokens(const void* O, int Hq, int T, int d, void* A, rmm_stream_t stream);
 
+/* ---------------------------------------------------------------- draft-tree decoding
+ *
+ * One decode step over a batch of sequences with trees of drafted tokens (or
+ * one token each): the projections of all nodes become heads with their norms
+ * and rotation and are appended to the caches (rmm_qkv_rope), the nodes attend
+ * to the cache and to their own ancestors (rmm_attn_tree), the logits become
+ * probabilities (rmm_softmax), the drafts are accepted or rejected against them
+ * (rmm_tree_verify), and the accepted nodes' keys and values stay
+ * (rmm_cache_keep).  The pages describe decoding one token at a time; these
+ * calls are the same reduced attention and layer glue for several.
+ *
+ * Common to them:
+ *   lens     int32 [B] on the device: each sequence's cached positions.  A
+ *            negative length marks an empty slot of the batch.  Sequence b's
+ *            nodes take the cache slots lens[b] .. lens[b]+T-1; one with
+ *            lens[b] > ldL - T has no room and is treated as an empty slot.
+ *   parents  int32 [B, T] on the device, T <= 64: node t hangs on
+ *            parents[b,t] in [0, t), or is a root (-1); any other value marks it
+ *            absent (padding), and a node below an absent one is absent.
+ *            NULL, where allowed: a chain, node t hangs on node t - 1.
+ * B <= 4096, at most 4096 heads of a kind (RMM_ERR_UNSUPPORTED above). */
+
+/* The q/k/v projections of B sequences of T tokens (token-major, as
+ * rmm_linear_group writes them) into the attention layouts, with per-head RMS
+ * norms and the position rotation, appending keys and values:
+ *   q, k:  x' = x / sqrt(mean_j x_j^2 + eps) * w   over the head's d dims, with
+ *          w = q_norm / k_norm (bf16 [d]; NULL: that norm is left out)
+ *   then   (x'_i, x'_j) -> (x'_i c - x'_j s, x'_j c + x'_i s),  c + is =
+ *          exp(i pos inv_freq[p]), for the pairs p < rot/2:
+ *          (i, j) = (p, p + rot/2), or (2p, 2p + 1) with interleaved != 0;
+ *          dims from rot on stay (inv_freq fp32 [rot/2]; NULL: no rotation)
+ *   Yq bf16 [B*T, Hq*d] -> Q [B, Hq, T, d]
+ *   Yk bf16 [B*T, Hkv*d] -> Kt [B, Hkv, d, ldL] at slot start + t
+ *   Yv bf16 [B*T, Hkv*d] -> V [B, Hkv, ldL, d] at slot start + t
+ * start = lens[b], or L0 for every sequence with lens NULL (then L0 >= 0 and
+ * L0 + T <= ldL); pos = start + t, or with parents start + the node's depth.
+ * Sums, angles and products are fp32 (angles fp64 until reduced), each output
+ * is rounded once.  Empty slots and absent nodes write nothing; other cache
+ * positions are not touched.  Requires d == 128, rot % 16 == 0 and rot <= d,
+ * ldL % 8 == 0, T <= 2^20, 16-byte aligned bf16 pointers. */
+rmm_status rmm_qkv_rope(const void* Yq, const void* Yk, const void* Yv, int B, int T, int Hq, int Hkv, int d,
+                        const void* q_norm, const void* k_norm, float eps, const float* inv_freq, int rot,
+                        int interleaved, const int32_t* lens, int L0, const int32_t* parents, void* Q, void* Kt,
+                        void* V, int ldL, rmm_stream_t stream);
+
+/* Workspace bytes needed by rmm_attn_tree for these sizes (0 for sizes or
+ * options that it refuses). */
+size_t rmm_attn_tree_workspace_bytes(int B, int Hq, int Hkv, int T, int ldL, int d, const rmm_options* options);
+
+/* Reduced attention of each sequence's nodes, batched over lengths: for each
+ * (sequence b, KV head g)
+ *   S = top-k of s_j = max over the group's query heads q and the present nodes t
+ *       of |Q[b,q,t,j]|   (k = ceil(r*d), ties to the lower index),
+ *   logit[q,t,l] = scale * sum_{j in S} Q[b,q,t,j] * Kt[b,g,j,l]
+ *       for the keys l < lens[b] and the slots lens[b] + a of node t and its
+ *       ancestors a,
+ *   O[b,q,t,:] = softmax_l(logit) . V[b,g,l,:]   (full d, fp32 softmax).
+ * Absent nodes and empty slots get O = 0 (their kept set entries in idx_out are
+ * left as they were for empty slots).  Key and value slots that no node sees
+ * may hold anything.  With T = 1 and parents NULL this is plain decoding of a
+ * batch of different lengths.
+ *   Q, O bf16 [B, Hq, T, d]; Kt bf16 [B, Hkv, d, ldL]; V bf16 [B, Hkv, ldL, d]
+ *   idx_out int32 [B, Hkv, k] or NULL
+ * A length without room (lens[b] > ldL - T) is reported through
+ * rmm_get_status() as RMM_ERR_INVALID_ARG.  Requirements: d == 128, T <= 64,
+ * Hq % Hkv == 0, T <= ldL, ldL % 8 == 0, 16-byte aligned pointers;
+ * options.attn_per_query_head and attn_path are not supported here. */
+rmm_status rmm_attn_tree(const void* Q, const void* Kt, const void* V, const int32_t* lens, const int32_t* parents,
+                         int B, int Hq, int Hkv, int T, int ldL, int d, double r, float scale, void* O,
+                         int32_t* idx_out, void* workspace, size_t workspace_bytes, rmm_stream_t stream,
+                         const rmm_options* options);
+
+/* Rows of logits as probabilities:
+ *   Y[i,v] = e^((X[i,v] - M_i) / temperature) / sum_w e^((X[i,w] - M_i) / temperature)
+ * with M_i the row's maximum; temperature 0 is the limit, 1 at the lowest index
+ * that holds M_i and 0 elsewhere (greedy decoding).  -inf logits get 0, a row of
+ * nothing else 0 everywhere; a NaN or +inf makes the row NaN at temperature > 0.
+ *   X bf16 [rows, V] with row stride ldx >= V elements, Y fp32 with row stride
+ *   ldy >= V (16-byte aligned rows are faster); V <= 262144, rows <= 2^24
+ *   temperature: 0, or within [1e-6, 1e6] */
+rmm_status rmm_softmax(const void* X, int rows, int V, int64_t ldx, float temperature, float* Y, int64_t ldy,
+                       rmm_stream_t stream);
+
+/* Drafted tokens checked against the target's probabilities with given random
+ * numbers.  Row (b, t) of P is the target's distribution after node t; row
+ * (b, t) of Qd the draft's distribution that node t's children were drawn from,
+ * independently (Qd NULL: the drafts are certain picks).  The walk starts at
+ * node 0 with R = P[b,0], Z = 1 and goes through the nodes in order; a child c
+ * of the current node v, holding token x, is
+ *   accepted when u[b,c] * q * Z < R(x), q = Qd[b,v,x] (1 without Qd): the walk
+ *     moves to c, R = P[b,c], Z = 1;
+ *   rejected otherwise: R = max(R - Z Qd[b,v], 0) (without Qd: R(x) = 0),
+ *     Z = sum R; a rejection that would leave nothing leaves R and Z alone.
+ * The next token is the lowest index v with R(0) + .. + R(v) > u[b,0] * sum R.
+ * R and the sums are fp64.
+ *   P, Qd   fp32 [B*T, V] with row strides ldp, ldq >= V; rows sum to 1; NaN and
+ *           negative values count as 0
+ *   tokens  int32 [B, T] (node 0's is not read; a node whose token is outside
+ *           [0, V) is passed over)
+ *   u       fp32 [B, T] in [0, 1): u[b,c] for node c's test, u[b,0] for the next token
+ *   path    int32 [B, T]: the accepted nodes, 0 first, then -1
+ *   emitted int32 [B, T]: the accepted nodes' tokens without node 0's, the next
+ *           token after them (-1 if P's row has no mass), then -1
+ *   count   int32 [B]: the nodes in path = the tokens in emitted
+ * A sequence whose node 0 is absent (parents[b,0] != -1) gets count 0 and -1.
+ * T <= 64, V <= 2^24. */
+rmm_status rmm_tree_verify(const float* P, int64_t ldp, const float* Qd, int64_t ldq, int B, int T, int V,
+                           const int32_t* tokens, const int32_t* parents, const float* u, int32_t* path,
+                           int32_t* emitted, int32_t* count, rmm_stream_t stream);
+
+/* The accepted nodes kept: in each of `count` caches (host arrays of device
+ * pointers; different caches, one per layer), the key and value at slot
+ * lens[b] + path[b,i] move to slot lens[b] + i for i < kept[b], and
+ * lens_out[b] = lens[b] + kept[b] (lens_out NULL: not written; it may be lens
+ * itself, and must not overlap it otherwise).
+ *   Kts[c] bf16 [B, Hkv, d, ldL], Vs[c] bf16 [B, Hkv, ldL, d], in place
+ *   path   int32 [B, T], ascending within the first kept[b] entries, in [0, T)
+ * A sequence with kept[b] outside [1, T], an empty slot or a path that is not
+ * ascending stays as it is, its length too.  d == 128, T <= 64, count <= 128. */
+rmm_status rmm_cache_keep(int count, void* const* Kts, void* const* Vs, int B, int Hkv, int d, int ldL,
+                          const int32_t* lens, const int32_t* path, const int32_t* kept, int T, int32_t* lens_out,
+                          rmm_stream_t stream);
+
 /* ---------------------------------------------------------------- self-test
  *
  * y[i] = 2^x[i] as the tensor-core attention's softmax computes half of its

@@ -9,6 +9,7 @@
 
 #include "rmm_common.cuh"
 #include "rmm_internal.h"
+#include "rmm_tree.cuh"
 
 namespace rmm {
 
@@ -702,6 +703,119 @@ rmm_status rmm_heads_to_tokens(const void* O, int Hq, int T, int d, void* A, rmm
     if (!aligned16(O) || !aligned16(A)) return RMM_ERR_INVALID_ARG;
     return cuda_status(launch_heads_to_tokens(static_cast<const uint16_t*>(O), Hq, T, static_cast<uint16_t*>(A),
                                               num_sms_current(), static_cast<cudaStream_t>(stream)));
+}
+
+// ---------------------------------------------------------------- draft-tree decoding
+
+rmm_status rmm_qkv_rope(const void* Yq, const void* Yk, const void* Yv, int B, int T, int Hq, int Hkv, int d,
+                        const void* q_norm, const void* k_norm, float eps, const float* inv_freq, int rot,
+                        int interleaved, const int32_t* lens, int L0, const int32_t* parents, void* Q, void* Kt,
+                        void* V, int ldL, rmm_stream_t stream) {
+    if (!Yq || !Yk || !Yv || !Q || !Kt || !V || B < 1 || T < 1 || Hq < 1 || Hkv < 1 || T > ldL || ldL % 8 != 0)
+        return RMM_ERR_INVALID_ARG;
+    if (!lens && (L0 < 0 || L0 > ldL - T)) return RMM_ERR_INVALID_ARG;
+    if ((q_norm || k_norm) && !(eps >= 0.0f && isfinite(eps))) return RMM_ERR_INVALID_ARG;
+    if (inv_freq && (rot < 1 || rot > d)) return RMM_ERR_INVALID_ARG;
+    if (!aligned16(Yq) || !aligned16(Yk) || !aligned16(Yv) || !aligned16(Q) || !aligned16(Kt) || !aligned16(V) ||
+        !aligned16(q_norm) || !aligned16(k_norm))
+        return RMM_ERR_INVALID_ARG;
+    if (d != 128 || (inv_freq && rot % 16 != 0) || (parents && T > kTreeMax) || Hq > kTreeMaxHeads ||
+        Hkv > kTreeMaxHeads || T > (1 << 20) || B > kTreeMaxBatch)
+        return RMM_ERR_UNSUPPORTED;
+    return cuda_status(launch_qkv_rope(
+        static_cast<const uint16_t*>(Yq), static_cast<const uint16_t*>(Yk), static_cast<const uint16_t*>(Yv), B, T, Hq,
+        Hkv, static_cast<const uint16_t*>(q_norm), static_cast<const uint16_t*>(k_norm), eps, inv_freq, rot,
+        interleaved ? 1 : 0, lens, L0, parents, static_cast<uint16_t*>(Q), static_cast<uint16_t*>(Kt),
+        static_cast<uint16_t*>(V), ldL, static_cast<cudaStream_t>(stream)));
+}
+
+namespace {
+
+bool attn_tree_sizes_ok(int B, int Hq, int Hkv, int T, int ldL) {
+    return B >= 1 && Hq >= 1 && Hkv >= 1 && T >= 1 && Hq % Hkv == 0 && ldL >= T && ldL % 8 == 0;
+}
+
+bool attn_tree_supported(int B, int Hq, int T, int d, const rmm_options& o) {
+    return d == 128 && T <= kTreeMax && Hq <= kTreeMaxHeads && B <= kTreeMaxBatch && !o.attn_per_query_head &&
+           o.attn_path == 0;
+}
+
+}  // namespace
+
+size_t rmm_attn_tree_workspace_bytes(int B, int Hq, int Hkv, int T, int ldL, int d, const rmm_options* options) {
+    if (!attn_tree_sizes_ok(B, Hq, Hkv, T, ldL) || !opts_valid(options) ||
+        !attn_tree_supported(B, Hq, T, d, opts_or_default(options)))
+        return 0;
+    return kStatusBytes + align_up((size_t)B * Hkv * d * sizeof(int32_t), kAlign) +
+           align_up(attn_tree_partial_bytes(B, Hq, Hkv, T, ldL, num_sms_current()), kAlign);
+}
+
+rmm_status rmm_attn_tree(const void* Q, const void* Kt, const void* V, const int32_t* lens, const int32_t* parents,
+                         int B, int Hq, int Hkv, int T, int ldL, int d, double r, float scale, void* O,
+                         int32_t* idx_out, void* workspace, size_t workspace_bytes, rmm_stream_t stream,
+                         const rmm_options* options) {
+    if (!Q || !Kt || !V || !lens || !O || !attn_tree_sizes_ok(B, Hq, Hkv, T, ldL) || !opts_valid(options))
+        return RMM_ERR_INVALID_ARG;
+    if (!aligned16(Q) || !aligned16(Kt) || !aligned16(V) || !aligned16(O)) return RMM_ERR_INVALID_ARG;
+    if (!(scale > 0.0f) || !isfinite(scale)) return RMM_ERR_INVALID_ARG;
+    if (!attn_tree_supported(B, Hq, T, d, opts_or_default(options))) return RMM_ERR_UNSUPPORTED;
+    const int k = rmm_k_for(d, r);
+    if (k < 1) return RMM_ERR_INVALID_ARG;
+    const int sms = num_sms_current();
+    // workspace: status | kept sets | split partials
+    const size_t idx_bytes = align_up((size_t)B * Hkv * d * sizeof(int32_t), kAlign);
+    const size_t need = kStatusBytes + idx_bytes + align_up(attn_tree_partial_bytes(B, Hq, Hkv, T, ldL, sms), kAlign);
+    if (!workspace || workspace_bytes < need || !aligned16(workspace)) return RMM_ERR_WORKSPACE;
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    return cuda_status(launch_attn_tree(
+        static_cast<const uint16_t*>(Q), static_cast<const uint16_t*>(Kt), static_cast<const uint16_t*>(V), B, Hq, Hkv,
+        T, ldL, k, scale, lens, parents, static_cast<uint16_t*>(O),
+        idx_out ? idx_out : reinterpret_cast<int32_t*>(ws + kStatusBytes),
+        reinterpret_cast<float*>(ws + kStatusBytes + idx_bytes), reinterpret_cast<int*>(ws), sms,
+        static_cast<cudaStream_t>(stream)));
+}
+
+rmm_status rmm_softmax(const void* X, int rows, int V, int64_t ldx, float temperature, float* Y, int64_t ldy,
+                       rmm_stream_t stream) {
+    if (!X || !Y || rows < 1 || V < 1 || ldx < V || ldy < V) return RMM_ERR_INVALID_ARG;
+    if (reinterpret_cast<uintptr_t>(X) % 2 != 0 || reinterpret_cast<uintptr_t>(Y) % 4 != 0) return RMM_ERR_INVALID_ARG;
+    if (temperature != 0.0f && !(temperature >= 1e-6f && temperature <= 1e6f)) return RMM_ERR_INVALID_ARG;
+    if (V > kSoftmaxMaxV || rows > (1 << 24)) return RMM_ERR_UNSUPPORTED;
+    return cuda_status(launch_softmax(static_cast<const uint16_t*>(X), rows, V, ldx, temperature, Y, ldy,
+                                      static_cast<cudaStream_t>(stream)));
+}
+
+rmm_status rmm_tree_verify(const float* P, int64_t ldp, const float* Qd, int64_t ldq, int B, int T, int V,
+                           const int32_t* tokens, const int32_t* parents, const float* u, int32_t* path,
+                           int32_t* emitted, int32_t* count, rmm_stream_t stream) {
+    if (!P || !tokens || !parents || !u || !path || !emitted || !count || B < 1 || T < 1 || V < 1 || ldp < V ||
+        (Qd && ldq < V))
+        return RMM_ERR_INVALID_ARG;
+    if (reinterpret_cast<uintptr_t>(P) % 4 != 0 || reinterpret_cast<uintptr_t>(Qd) % 4 != 0) return RMM_ERR_INVALID_ARG;
+    if (T > kTreeMax || V > kVerifyMaxV || B > kTreeMaxBatch) return RMM_ERR_UNSUPPORTED;
+    return cuda_status(launch_tree_verify(P, ldp, Qd, ldq, B, T, V, tokens, parents, u, path, emitted, count,
+                                          static_cast<cudaStream_t>(stream)));
+}
+
+rmm_status rmm_cache_keep(int count, void* const* Kts, void* const* Vs, int B, int Hkv, int d, int ldL,
+                          const int32_t* lens, const int32_t* path, const int32_t* kept, int T, int32_t* lens_out,
+                          rmm_stream_t stream) {
+    if (!Kts || !Vs || !lens || !path || !kept || count < 1 || B < 1 || Hkv < 1 || T < 1 || T > ldL || ldL % 8 != 0)
+        return RMM_ERR_INVALID_ARG;
+    if (d != 128 || T > kTreeMax || count > kMaxCaches || B > kTreeMaxBatch || Hkv > kTreeMaxHeads)
+        return RMM_ERR_UNSUPPORTED;
+    // lens_out is lens itself, or apart from it
+    if (lens_out && lens_out != lens && lens_out < lens + B && lens < lens_out + B) return RMM_ERR_INVALID_ARG;
+    CacheList c;
+    for (int i = 0; i < count; ++i) {
+        if (!Kts[i] || !Vs[i] || !aligned16(Kts[i]) || !aligned16(Vs[i])) return RMM_ERR_INVALID_ARG;
+        for (int j = 0; j < i; ++j)  // one cache twice would be moved twice
+            if (Kts[i] == Kts[j] || Vs[i] == Vs[j]) return RMM_ERR_INVALID_ARG;
+        c.Kt[i] = static_cast<uint16_t*>(Kts[i]);
+        c.V[i] = static_cast<uint16_t*>(Vs[i]);
+    }
+    return cuda_status(launch_cache_keep(c, count, B, Hkv, ldL, lens, path, kept, T, lens_out,
+                                         static_cast<cudaStream_t>(stream)));
 }
 
 rmm_status rmm_selftest_exp2_fma(const float* x, float* y, int n, rmm_stream_t stream) {

@@ -185,6 +185,35 @@ cudaError_t launch_attn_ctx(const uint16_t* Q, const uint16_t* Kt, const uint16_
                             int per_query_head, uint16_t* O, int32_t* idx, uint32_t* sc, uint32_t* keys,
                             int32_t* blocks, float* partials, const AttnPlan& p, cudaStream_t stream);
 
+// ---- draft-tree decoding: heads with norms and rotation (rmm_rope.cu), tree
+// attention (rmm_attn_tree.cu), probabilities (rmm_softmax.cu), verification
+// (rmm_verify.cu), kept nodes (rmm_keep.cu)
+cudaError_t launch_qkv_rope(const uint16_t* Yq, const uint16_t* Yk, const uint16_t* Yv, int B, int T, int Hq, int Hkv,
+                            const uint16_t* q_norm, const uint16_t* k_norm, float eps, const float* inv_freq, int rot,
+                            int interleaved, const int32_t* lens, int L0, const int32_t* parents, uint16_t* Q,
+                            uint16_t* Kt, uint16_t* V, int ldL, cudaStream_t stream);
+// Bytes of split partials for these sizes.
+size_t attn_tree_partial_bytes(int B, int Hq, int Hkv, int T, int ldL, int num_sms);
+// idx: int32 [B * Hkv * k], written (the kept dims of each set).
+cudaError_t launch_attn_tree(const uint16_t* Q, const uint16_t* Kt, const uint16_t* V, int B, int Hq, int Hkv, int T,
+                             int ldL, int k, float scale, const int32_t* lens, const int32_t* parents, uint16_t* O,
+                             int32_t* idx, float* partials, int* status, int num_sms, cudaStream_t stream);
+constexpr int kSoftmaxMaxV = 262144;  // logits per row
+cudaError_t launch_softmax(const uint16_t* X, int rows, int V, int64_t ldx, float temperature, float* Y, int64_t ldy,
+                           cudaStream_t stream);
+constexpr int kVerifyMaxV = 1 << 24;
+cudaError_t launch_tree_verify(const float* P, int64_t ldp, const float* Qd, int64_t ldq, int B, int T, int V,
+                               const int32_t* tokens, const int32_t* parents, const float* u, int32_t* path,
+                               int32_t* emitted, int32_t* count, cudaStream_t stream);
+constexpr int kMaxCaches = 128;  // caches per keep call
+struct CacheList {
+    uint16_t* Kt[kMaxCaches];
+    uint16_t* V[kMaxCaches];
+};
+cudaError_t launch_cache_keep(const CacheList& caches, int ncaches, int B, int Hkv, int ldL, const int32_t* lens,
+                              const int32_t* path, const int32_t* count, int T, int32_t* lens_out,
+                              cudaStream_t stream);
+
 // ---- glue (rmm_glue.cu)
 cudaError_t launch_transpose(const uint16_t* W, uint16_t* Wt, int N, int H, cudaStream_t stream);
 // src null: the identity list 0..k-1 (every slice kept); dst_copy (if not

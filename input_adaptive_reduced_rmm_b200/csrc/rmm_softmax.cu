@@ -1,0 +1,204 @@
+// rmm_softmax.cu -- rows of logits as probabilities at a temperature:
+//   y_i = e^((x_i - M) / t) / sum_j e^((x_j - M) / t),   M = max_j x_j
+// bf16 in, fp32 out; at temperature 0 the limit, 1 at the lowest index of M.
+//
+// Memory bound: 2 bytes read and 4 written per element.  A row belongs to a
+// cluster of 1, 2, 4 or 8 CTAs, each of which keeps its part of the row in
+// registers between the passes, so the row is read once.  Each CTA forms its
+// own maximum and its sum relative to that; one exchange of these pairs through
+// distributed shared memory gives the row's maximum and sum.
+#include <math.h>
+
+#include "rmm_common.cuh"
+#include "rmm_internal.h"
+
+namespace rmm {
+
+namespace {
+
+constexpr int kThreads = 512;
+constexpr float kLog2e = 1.4426950408889634f;
+
+__device__ __forceinline__ float ld_shared_cluster_f32(uint32_t addr) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+// Merge (m, s): the maximum of two parts, the sum relative to it.  Parts without
+// a finite or infinite element have m = -inf and s = 0.
+__device__ __forceinline__ void merge(float& m, float& s, float m2, float s2, float c) {
+    const float mm = fmaxf(m, m2);
+    const float a = m == mm ? s : s * exp2f((m - mm) * c);
+    const float b = m2 == mm ? s2 : s2 * exp2f((m2 - mm) * c);
+    m = mm;
+    s = a + b;
+}
+
+// NV: 16-byte vectors (8 logits) per thread.  wide: rows of X start on 16-byte
+// boundaries; wide_y: rows of Y do.
+template <int NV>
+__global__ void __launch_bounds__(kThreads)
+    softmax_kernel(const uint16_t* __restrict__ X, int V, int64_t ldx, float c, int one_hot, float* __restrict__ Y,
+                   int64_t ldy, int nc, int wide, int wide_y) {
+    __shared__ float red_m[kThreads / 32], red_s[kThreads / 32];
+    __shared__ int red_i[kThreads / 32];
+    __shared__ float part[2];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int64_t row = blockIdx.x / nc;
+    const int rank = blockIdx.x % nc;
+    const uint16_t* x = X + row * ldx;
+    const int v0 = rank * (NV * kThreads);  // first vector of this CTA
+    pdl_wait();
+    pdl_launch_dependents();
+    uint4 r[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int e0 = (v0 + i * kThreads + tid) * 8;
+        if (wide && e0 + 8 <= V) {
+            r[i] = ld_nc_v4(x + e0);
+        } else {
+            uint32_t w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {  // -inf past the row's end
+                const uint32_t lo = e0 + 2 * e < V ? x[e0 + 2 * e] : 0xFF80u;
+                const uint32_t hi = e0 + 2 * e + 1 < V ? x[e0 + 2 * e + 1] : 0xFF80u;
+                w[e] = lo | (hi << 16);
+            }
+            r[i] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+    }
+    auto at = [&](int i, int e) -> float {
+        const uint32_t w = e < 2 ? r[i].x : e < 4 ? r[i].y : e < 6 ? r[i].z : r[i].w;
+        return __uint_as_float((e & 1) ? w & 0xFFFF0000u : w << 16);
+    };
+    float m = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) m = fmaxf(m, at(i, e));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if (lane == 0) red_m[warp] = m;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) m = fmaxf(m, red_m[w]);
+
+    if (one_hot) {
+        // the lowest index that holds the CTA's maximum, then the row's
+        int best = 0x7FFFFFFF;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int e = 7; e >= 0; --e)
+                if (at(i, e) == m) best = min(best, (v0 + i * kThreads + tid) * 8 + e);
+        best = __reduce_min_sync(0xffffffffu, best);
+        if (lane == 0) red_i[warp] = best;
+        __syncthreads();
+        for (int w = 0; w < kThreads / 32; ++w) best = min(best, red_i[w]);
+        if (nc > 1) {
+            if (tid == 0) part[0] = m, part[1] = __int_as_float(best);
+            cluster_sync();
+            float M = -INFINITY;
+            for (int j = 0; j < nc; ++j) M = fmaxf(M, ld_shared_cluster_f32(mapa_shared(smem_addr(&part[0]), j)));
+            best = 0x7FFFFFFF;
+            for (int j = 0; j < nc; ++j)
+                if (ld_shared_cluster_f32(mapa_shared(smem_addr(&part[0]), j)) == M)
+                    best = min(best, __float_as_int(ld_shared_cluster_f32(mapa_shared(smem_addr(&part[1]), j))));
+            m = M;
+            cluster_sync();
+        }
+        if (m == -INFINITY) best = -1;  // nothing but -inf: no probability anywhere
+        float* y = Y + row * ldy;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int e0 = (v0 + i * kThreads + tid) * 8;
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (e0 + e < V) y[e0 + e] = e0 + e == best ? 1.0f : 0.0f;
+        }
+        return;
+    }
+
+    float s = 0.f;
+    if (m > -INFINITY) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) s += exp2f((at(i, e) - m) * c);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (lane == 0) red_s[warp] = s;
+    __syncthreads();
+    s = 0.f;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) s += red_s[w];
+    if (nc > 1) {
+        if (tid == 0) part[0] = m, part[1] = s;
+        cluster_sync();
+        m = -INFINITY, s = 0.f;
+        for (int j = 0; j < nc; ++j)
+            merge(m, s, ld_shared_cluster_f32(mapa_shared(smem_addr(&part[0]), j)),
+                  ld_shared_cluster_f32(mapa_shared(smem_addr(&part[1]), j)), c);
+        cluster_sync();  // no CTA leaves while another still reads its pair
+    }
+    const float inv = 1.0f / s;
+    float* y = Y + row * ldy;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int e0 = (v0 + i * kThreads + tid) * 8;
+        if (e0 >= V) continue;
+        float p[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) p[e] = m > -INFINITY ? exp2f((at(i, e) - m) * c) * inv : 0.0f;
+        if (wide_y && e0 + 8 <= V) {
+            *reinterpret_cast<float4*>(y + e0) = make_float4(p[0], p[1], p[2], p[3]);
+            *reinterpret_cast<float4*>(y + e0 + 4) = make_float4(p[4], p[5], p[6], p[7]);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (e0 + e < V) y[e0 + e] = p[e];
+        }
+    }
+}
+
+template <int NV>
+cudaError_t launch(const uint16_t* X, int rows, int V, int64_t ldx, float temperature, float* Y, int64_t ldy, int nc,
+                   cudaStream_t stream) {
+    const int wide = (reinterpret_cast<uintptr_t>(X) & 15) == 0 && ldx % 8 == 0;
+    const int wide_y = (reinterpret_cast<uintptr_t>(Y) & 15) == 0 && ldy % 4 == 0;
+    const int one_hot = temperature == 0.0f;
+    const float c = one_hot ? 0.0f : kLog2e / temperature;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)rows * nc);
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = nc;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, softmax_kernel<NV>, X, V, ldx, c, one_hot, Y, ldy, nc, wide, wide_y);
+}
+
+}  // namespace
+
+cudaError_t launch_softmax(const uint16_t* X, int rows, int V, int64_t ldx, float temperature, float* Y, int64_t ldy,
+                           cudaStream_t stream) {
+    const int vecs = (V + 7) / 8;
+    int nc = 1;
+    while (nc < 8 && vecs > nc * kThreads) nc *= 2;
+    const int nv = (vecs + nc * kThreads - 1) / (nc * kThreads);
+    if (nv <= 1) return launch<1>(X, rows, V, ldx, temperature, Y, ldy, nc, stream);
+    if (nv <= 2) return launch<2>(X, rows, V, ldx, temperature, Y, ldy, nc, stream);
+    if (nv <= 4) return launch<4>(X, rows, V, ldx, temperature, Y, ldy, nc, stream);
+    if (nv <= 8) return launch<8>(X, rows, V, ldx, temperature, Y, ldy, nc, stream);
+    return cudaErrorInvalidValue;
+}
+
+}  // namespace rmm

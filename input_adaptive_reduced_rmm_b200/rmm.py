@@ -31,6 +31,8 @@ EXPORTED = (
     "rmm_linear_decode_noalloc", "rmm_linear_group", "rmm_linear_group_workspace_bytes",
     "rmm_add_rmsnorm", "rmm_swiglu", "rmm_qkv_heads", "rmm_heads_to_tokens",
     "rmm_ctx_block_means", "rmm_attn_ctx_workspace_bytes", "rmm_attn_ctx", "rmm_selftest_exp2_fma",
+    "rmm_qkv_rope", "rmm_attn_tree_workspace_bytes", "rmm_attn_tree", "rmm_softmax", "rmm_tree_verify",
+    "rmm_cache_keep",
 )
 
 
@@ -116,6 +118,12 @@ def lib() -> ctypes.CDLL:
         "rmm_attn_ctx_workspace_bytes": (Z, [I, I, I, I, I, I, I, D, OP]),
         "rmm_attn_ctx": (I, [P, P, P, P, I, I, I, I, I, I, I, D, D, I, I, F, P, P, P, P, Z, P, OP]),
         "rmm_selftest_exp2_fma": (I, [P, P, I, P]),
+        "rmm_qkv_rope": (I, [P, P, P, I, I, I, I, I, P, P, F, P, I, I, P, I, P, P, P, P, I, P]),
+        "rmm_attn_tree_workspace_bytes": (Z, [I, I, I, I, I, I, OP]),
+        "rmm_attn_tree": (I, [P, P, P, P, P, I, I, I, I, I, I, D, F, P, P, P, Z, P, OP]),
+        "rmm_softmax": (I, [P, I, I, ctypes.c_int64, F, P, ctypes.c_int64, P]),
+        "rmm_tree_verify": (I, [P, ctypes.c_int64, P, ctypes.c_int64, I, I, I, P, P, P, P, P, P, P]),
+        "rmm_cache_keep": (I, [I, P, P, I, I, I, I, P, P, P, I, P, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(L, name)
@@ -523,3 +531,203 @@ def rmm_selftest_exp2_fma(x: torch.Tensor, y: torch.Tensor | None = None, stream
     _on_cuda(x=x, y=y)
     _check(lib().rmm_selftest_exp2_fma(_ptr(x), _ptr(y), x.numel(), _stream(stream)), "rmm_selftest_exp2_fma")
     return y
+
+
+# ---------------------------------------------------------------- draft-tree decoding
+
+TREE_MAX = 64  # nodes per tree
+
+
+def _here(**tensors):
+    """Every tensor on the current CUDA device: the kernels are launched there."""
+    dev = None
+    for name, t in tensors.items():
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        if dev is None:
+            dev = torch.cuda.current_device()
+        if t.device.index != dev:
+            raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
+
+
+def _new(shape, dtype, like, stream):
+    """An output allocated for the stream that writes it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=like.device)
+
+
+def _caches(Kt, V):
+    _dims(Kt, "Kt", 4)
+    B, Hkv, d, ldL = Kt.shape
+    _need(Kt, "Kt")
+    _need(V, "V", shape=(B, Hkv, ldL, d))
+    return B, Hkv, d, ldL
+
+
+def rmm_qkv_rope(Yq: torch.Tensor, Yk: torch.Tensor, Yv: torch.Tensor, Q: torch.Tensor, Kt: torch.Tensor,
+                 V: torch.Tensor, lens: torch.Tensor | None = None, L0: int = 0,
+                 parents: torch.Tensor | None = None, q_norm: torch.Tensor | None = None,
+                 k_norm: torch.Tensor | None = None, eps: float = 1e-6, inv_freq: torch.Tensor | None = None,
+                 interleaved: bool = False, stream=None) -> torch.Tensor:
+    """Token-major q/k/v of B sequences -> Q [B,Hq,T,d] and the caches Kt [B,Hkv,d,ldL], V [B,Hkv,ldL,d], with
+    per-head RMS norms (q_norm, k_norm bf16 [d]) and the rotation by position (inv_freq fp32 [rot/2]).  Sequence
+    b is appended at lens[b] (int32 [B]), or all of them at L0; with parents (int32 [B,T]) a node's position is
+    its depth in the tree past that.  Yq [B*T, Hq*d], Yk and Yv [B*T, Hkv*d].  Returns Q."""
+    _dims(Q, "Q", 4)
+    B, Hq, T, d = Q.shape
+    Bk, Hkv, dk, ldL = _caches(Kt, V)
+    if Bk != B or dk != d:
+        raise ValueError("Q and the caches disagree on the batch or the head dimension")
+    _need(Q, "Q")
+    _need(Yq, "Yq", shape=(B * T, Hq * d))
+    _need(Yk, "Yk", shape=(B * T, Hkv * d))
+    _need(Yv, "Yv", shape=(B * T, Hkv * d))
+    _need(lens, "lens", torch.int32, shape=(B,))
+    _need(parents, "parents", torch.int32, shape=(B, T))
+    _need(q_norm, "q_norm", shape=(d,))
+    _need(k_norm, "k_norm", shape=(d,))
+    rot = 0
+    if inv_freq is not None:
+        _dims(inv_freq, "inv_freq", 1)
+        _need(inv_freq, "inv_freq", torch.float32)
+        rot = 2 * inv_freq.numel()
+    _here(Yq=Yq, Yk=Yk, Yv=Yv, Q=Q, Kt=Kt, V=V, lens=lens, parents=parents, q_norm=q_norm, k_norm=k_norm,
+          inv_freq=inv_freq)
+    _check(lib().rmm_qkv_rope(_ptr(Yq), _ptr(Yk), _ptr(Yv), B, T, Hq, Hkv, d, _ptr(q_norm), _ptr(k_norm), float(eps),
+                              _ptr(inv_freq), rot, int(bool(interleaved)), _ptr(lens), int(L0), _ptr(parents),
+                              _ptr(Q), _ptr(Kt), _ptr(V), ldL, _stream(stream)), "rmm_qkv_rope")
+    return Q
+
+
+def rmm_attn_tree_workspace_bytes(B: int, Hq: int, Hkv: int, T: int, ldL: int, d: int = 128,
+                                  opts: rmm_options | None = None) -> int:
+    return int(lib().rmm_attn_tree_workspace_bytes(int(B), int(Hq), int(Hkv), int(T), int(ldL), int(d), _opt(opts)))
+
+
+def rmm_attn_tree(Q: torch.Tensor, Kt: torch.Tensor, V: torch.Tensor, lens: torch.Tensor, r: float,
+                  parents: torch.Tensor | None = None, scale: float | None = None, O: torch.Tensor | None = None,
+                  idx_out: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                  opts: rmm_options | None = None, stream=None) -> torch.Tensor:
+    """Reduced attention of T <= 64 nodes per sequence (a tree by parents int32 [B,T], a chain without) over each
+    sequence's lens[b] cached keys and the node's own ancestors, whose keys sit at the slots lens[b] + node.
+    Q [B,Hq,T,d]; Kt [B,Hkv,d,ldL]; V [B,Hkv,ldL,d]; lens int32 [B] (negative: an empty slot, O = 0);
+    idx_out (optional) int32 with room for [B, Hkv, ceil(r*d)]."""
+    _dims(Q, "Q", 4)
+    B, Hq, T, d = Q.shape
+    Bk, Hkv, dk, ldL = _caches(Kt, V)
+    if Bk != B or dk != d:
+        raise ValueError("Q and the caches disagree on the batch or the head dimension")
+    _need(Q, "Q")
+    _need(lens, "lens", torch.int32, shape=(B,))
+    _need(parents, "parents", torch.int32, shape=(B, T))
+    _need(O, "O", shape=(B, Hq, T, d))
+    if idx_out is not None:
+        _need(idx_out, "idx_out", torch.int32, min_numel=B * Hkv * max(0, rmm_k_for(d, r)))
+    _here(Q=Q, Kt=Kt, V=V, lens=lens, parents=parents, O=O, idx_out=idx_out, workspace=workspace)
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    if O is None:
+        O = _new((B, Hq, T, d), torch.bfloat16, Q, stream)
+    if workspace is None:
+        n = rmm_attn_tree_workspace_bytes(B, Hq, Hkv, T, ldL, d, opts)
+        workspace = _new((max(n, 256),), torch.uint8, Q, stream)
+        rmm_workspace_init(workspace, stream)
+    _check(lib().rmm_attn_tree(_ptr(Q), _ptr(Kt), _ptr(V), _ptr(lens), _ptr(parents), B, Hq, Hkv, T, ldL, d, float(r),
+                               float(scale), _ptr(O), _ptr(idx_out), _ptr(workspace), workspace.numel(),
+                               _stream(stream), _opt(opts)), "rmm_attn_tree")
+    return O
+
+
+def _rows(t, name, dtype, rows=None, V=None):
+    """A 2-D tensor whose rows are contiguous (their stride may be larger than V): its row stride."""
+    if t.dtype != dtype or t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be a 2-D {dtype} tensor with contiguous rows")
+    if rows is not None and tuple(t.shape) != (rows, V):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(rows, V)}")
+    ld = t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    if ld < t.shape[1]:
+        raise ValueError(f"{name} has overlapping rows")
+    return ld
+
+
+def rmm_softmax(X: torch.Tensor, temperature: float = 1.0, Y: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Rows of bf16 logits [rows, V] (row stride free) -> probabilities fp32 at a temperature; 0 is greedy: 1 at
+    the lowest index of the row's maximum."""
+    ldx = _rows(X, "X", torch.bfloat16)
+    rows, V = X.shape
+    ldy = _rows(Y, "Y", torch.float32, rows, V) if Y is not None else V
+    _here(X=X, Y=Y)
+    if Y is None:
+        Y = _new((rows, V), torch.float32, X, stream)
+    _check(lib().rmm_softmax(_ptr(X), rows, V, ldx, float(temperature), _ptr(Y), ldy, _stream(stream)), "rmm_softmax")
+    return Y
+
+
+def rmm_tree_verify(P: torch.Tensor, tokens: torch.Tensor, parents: torch.Tensor, u: torch.Tensor,
+                    Qd: torch.Tensor | None = None, path: torch.Tensor | None = None,
+                    emitted: torch.Tensor | None = None, count: torch.Tensor | None = None, stream=None):
+    """Drafted tokens (int32 [B,T], a tree by parents [B,T]) accepted or rejected against the target's
+    probabilities P (fp32 [B,T,V], or [B*T,V] with a row stride) with the random numbers u (fp32 [B,T]); Qd, like
+    P, are the draft's rows that the children of each node were drawn from (None: certain picks).
+    Returns (path [B,T], emitted [B,T], count [B]): the accepted nodes, their tokens and the next one, how many."""
+    _dims(tokens, "tokens", 2)
+    B, T = tokens.shape
+    _need(tokens, "tokens", torch.int32)
+    _need(parents, "parents", torch.int32, shape=(B, T))
+    _need(u, "u", torch.float32, shape=(B, T))
+    if P.dim() == 3:
+        P = P.flatten(0, 1) if P.is_contiguous() else P
+    V = P.shape[-1]
+    ldp = _rows(P, "P", torch.float32, B * T, V)
+    ldq = 0
+    if Qd is not None:
+        if Qd.dim() == 3:
+            Qd = Qd.flatten(0, 1) if Qd.is_contiguous() else Qd
+        ldq = _rows(Qd, "Qd", torch.float32, B * T, V)
+    _need(path, "path", torch.int32, shape=(B, T))
+    _need(emitted, "emitted", torch.int32, shape=(B, T))
+    _need(count, "count", torch.int32, shape=(B,))
+    _here(P=P, tokens=tokens, parents=parents, u=u, Qd=Qd, path=path, emitted=emitted, count=count)
+    if path is None:
+        path = _new((B, T), torch.int32, tokens, stream)
+    if emitted is None:
+        emitted = _new((B, T), torch.int32, tokens, stream)
+    if count is None:
+        count = _new((B,), torch.int32, tokens, stream)
+    _check(lib().rmm_tree_verify(_ptr(P), ldp, _ptr(Qd), ldq, B, T, V, _ptr(tokens), _ptr(parents), _ptr(u),
+                                 _ptr(path), _ptr(emitted), _ptr(count), _stream(stream)), "rmm_tree_verify")
+    return path, emitted, count
+
+
+def rmm_cache_keep(caches, lens: torch.Tensor, path: torch.Tensor, count: torch.Tensor,
+                   lens_out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Keep the accepted nodes in every cache (a list of (Kt [B,Hkv,d,ldL], V [B,Hkv,ldL,d]) pairs, one per
+    layer): slot lens[b] + path[b,i] moves to lens[b] + i for i < count[b].  Returns lens + count in lens_out
+    (new by default; lens itself updates it in place)."""
+    caches = list(caches)
+    if not caches:
+        raise ValueError("no cache given")
+    B, Hkv, d, ldL = _caches(*caches[0])
+    for Kt, V in caches:
+        _need(Kt, "Kt", shape=(B, Hkv, d, ldL))
+        _need(V, "V", shape=(B, Hkv, ldL, d))
+        _here(Kt=Kt, V=V)
+    _dims(path, "path", 2)
+    T = path.shape[1]
+    _need(path, "path", torch.int32, shape=(B, T))
+    _need(lens, "lens", torch.int32, shape=(B,))
+    _need(count, "count", torch.int32, shape=(B,))
+    _need(lens_out, "lens_out", torch.int32, shape=(B,))
+    _here(lens=lens, path=path, count=count, lens_out=lens_out)
+    if lens_out is None:
+        lens_out = _new((B,), torch.int32, lens, stream)
+    n = len(caches)
+    kt = (ctypes.c_void_p * n)(*[Kt.data_ptr() for Kt, _ in caches])
+    v = (ctypes.c_void_p * n)(*[V.data_ptr() for _, V in caches])
+    _check(lib().rmm_cache_keep(n, kt, v, B, Hkv, d, ldL, _ptr(lens), _ptr(path), _ptr(count), T, _ptr(lens_out),
+                                _stream(stream)), "rmm_cache_keep")
+    return lens_out
