@@ -432,6 +432,7 @@ rmm_status rmm_softmax(const void* X, int rows, int V, int64_t ldx, float temper
  *   tokens  int32 [B, T] (node 0's is not read; a node whose token is outside
  *           [0, V) is passed over)
  *   u       fp32 [B, T] in [0, 1): u[b,c] for node c's test, u[b,0] for the next token
+ *           (there NaN counts as 0, and from 1 on it is the last token with mass)
  *   path    int32 [B, T]: the accepted nodes, 0 first, then -1
  *   emitted int32 [B, T]: the accepted nodes' tokens without node 0's, the next
  *           token after them (-1 if P's row has no mass), then -1

@@ -145,7 +145,7 @@ def verify(P, tokens, parents, u, Qd=None):
                 R, Z = rest, float(rest.sum())
         run = torch.cumsum(R, 0)
         if float(run[-1]) > 0.0:
-            goal = max(uu[0], 0.0) * float(run[-1])
+            goal = (uu[0] if uu[0] > 0.0 else 0.0) * float(run[-1])  # NaN counts as 0
             over = torch.nonzero((run > goal) & (R > 0))
             nxt = int(over[0]) if len(over) else int(torch.nonzero(R > 0)[-1])
         else:
