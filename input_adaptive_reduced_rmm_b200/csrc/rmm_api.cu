@@ -736,8 +736,9 @@ bool attn_tree_sizes_ok(int B, int Hq, int Hkv, int T, int ldL) {
 }
 
 bool attn_tree_supported(int B, int Hq, int T, int d, const rmm_options& o) {
-    return d == 128 && T <= kTreeMax && Hq <= kTreeMaxHeads && B <= kTreeMaxBatch && !o.attn_per_query_head &&
-           o.attn_path == 0;
+    // (rows of queries and of K^T are int coordinates of the tensor maps)
+    return d == 128 && T <= kTreeMax && Hq <= kTreeMaxHeads && B <= kTreeMaxBatch && (int64_t)B * Hq < (1 << 24) &&
+           !o.attn_per_query_head && o.attn_path == 0;
 }
 
 }  // namespace
@@ -767,12 +768,22 @@ rmm_status rmm_attn_tree(const void* Q, const void* Kt, const void* V, const int
     const size_t need = kStatusBytes + idx_bytes + align_up(attn_tree_partial_bytes(B, Hq, Hkv, T, ldL, sms), kAlign);
     if (!workspace || workspace_bytes < need || !aligned16(workspace)) return RMM_ERR_WORKSPACE;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
-    return cuda_status(launch_attn_tree(
-        static_cast<const uint16_t*>(Q), static_cast<const uint16_t*>(Kt), static_cast<const uint16_t*>(V), B, Hq, Hkv,
-        T, ldL, k, scale, lens, parents, static_cast<uint16_t*>(O),
-        idx_out ? idx_out : reinterpret_cast<int32_t*>(ws + kStatusBytes),
-        reinterpret_cast<float*>(ws + kStatusBytes + idx_bytes), reinterpret_cast<int*>(ws), sms,
-        static_cast<cudaStream_t>(stream)));
+    const uint64_t planes = (uint64_t)B * Hkv;
+    CUtensorMap qm, km, vm;
+    try {
+        if (!tiled_map(Q, (uint64_t)B * Hq * T, d, d, 128, &qm) ||
+            !(k == d ? tiled_map_3d(Kt, ldL, d, planes, ldL, (uint64_t)d * ldL, 128, &km)
+                     : row_gather_map(Kt, planes * d, ldL, ldL, &km)) ||
+            !tiled_map_3d(V, d, ldL, planes, d, (uint64_t)d * ldL, 128, &vm))
+            return RMM_ERR_CUDA;
+    } catch (...) {  // the maps' cache is out of memory
+        return RMM_ERR_CUDA;
+    }
+    return cuda_status(launch_attn_tree(qm, km, vm, static_cast<const uint16_t*>(Q), B, Hq, Hkv, T, ldL, k, scale, lens,
+                                        parents, static_cast<uint16_t*>(O),
+                                        idx_out ? idx_out : reinterpret_cast<int32_t*>(ws + kStatusBytes),
+                                        idx_out != nullptr, ws + kStatusBytes + idx_bytes, reinterpret_cast<int*>(ws),
+                                        sms, static_cast<cudaStream_t>(stream)));
 }
 
 rmm_status rmm_softmax(const void* X, int rows, int V, int64_t ldx, float temperature, float* Y, int64_t ldy,

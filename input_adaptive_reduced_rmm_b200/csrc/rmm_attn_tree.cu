@@ -1,13 +1,47 @@
-// rmm_attn_tree.cu -- reduced attention of a draft tree over the cache.
+// rmm_attn_tree.cu -- reduced attention of draft trees over the caches of a
+// batch of sequences with their own lengths, on the tensor cores.
 //
 // Sequence b has len_b cached keys and T <= 64 tree nodes whose keys sit at the
-// slots len_b .. len_b + T - 1.  For KV head g with its G query heads q:
-//   S     = the k dims with the largest max over q and the present t of |Q[q,t,j]|
-//   x_l   = scale * sum_{j in S} Q[q,t,j] K[l,j]   for l < len_b and for the slots
-//           of node t and its ancestors
-//   O     = softmax(x) V, zero where the row sees no key
-// One CTA per (sequence, query head, node): 128 keys at a time, a thread per key
-// for the logits, a thread per dim for P.V, with the running maximum and sum.
+// slots len_b .. len_b + T - 1.  For KV head g, its G query heads and T nodes
+// stack into R = G T rows that share every key and value:
+//   S   = the k dims with the largest max over the present rows of |Q[row,j]|
+//   x_l = scale * sum_{j in S} Q[row,j] K[l,j]     for l < len_b and for the slots
+//         of the row's node and its ancestors
+//   O   = softmax(x) V, zero where the row sees no key
+//
+// What bounds it: K^T (its kept rows) and V are read once per (sequence, KV
+// head), 2 (k + 128) bytes a key, against 2 R (k + 128) products a key: memory
+// up to about R = 250 rows, the tensor cores and the softmax beyond.  So the rows
+// are stacked, up to 256 to a CTA, and the keys are split.
+//
+// Work: a unit is (sequence, KV head, pair of 128-row tiles); its keys come in
+// blocks of 128.  All units' blocks, in order, are cut into equal shares, one per
+// CTA (one CTA per SM), wherever the cuts fall: ragged batches balance and few
+// units still fill the GPU.  A unit inside one share is finished there; one that
+// was cut leaves fp32 partials (maximum, sum, unnormalised output), at most two
+// per CTA, which a second kernel joins.  Lengths are read on the device only, so
+// a captured call serves any lengths.
+//
+// Two softmax groups of four warps (a thread per row) alternate on the tensor
+// cores: with two row tiles each group has its own tile and both use every key
+// block; with one, the groups take alternate key blocks of the same rows, each
+// with its own maximum, sum and output, joined at the end of the unit.
+//
+//   warps 0-7  softmax: S from TMEM, mask, running maximum, P (bf16) over S's own
+//              columns, O rescaled only when the maximum grew by more than 2^8;
+//              the query operand at the start of a unit, its output at the end
+//   warp 8     MMA: S = Q_S K_S^T for a group's next step as soon as its P.V is
+//              done, P.V (A from TMEM) as soon as its P is written
+//   warp 9     TMA: key and value blocks through two rings, running ahead over
+//              units.  With every dim kept the key block is two tile copies of
+//              the d-major cache; else the kept rows come by tile::gather4.
+//
+// Operands in shared memory are 128-byte swizzled: K and V MN-major as the
+// caches lay them out, Q K-major (a tile copy) or, gathered, MN-major.  TMEM
+// holds S0, S1, O0, O1 (128 columns each).  Value rows past a sequence's slots
+// are zeroed in shared memory before P.V: 0 times what they hold could be NaN.
+// Every wait is bounded: on expiry the kernel records RMM_ERR_TIMEOUT, all roles
+// leave their loops, copies and MMAs in flight drain, TMEM is freed.
 #include <math.h>
 
 #include "rmm_common.cuh"
@@ -19,108 +53,754 @@ namespace rmm {
 namespace {
 
 constexpr int D = 128;
+constexpr int BM = 128;  // rows per tile (= TMEM lanes)
+constexpr int BK = 128;  // keys per block
+constexpr int kMaxStages = 6;
+constexpr int kSoftmaxThreads = 256;
+constexpr int kMmaWarp = 8, kTmaWarp = 9;
+constexpr int kThreadsTree = 320;
+constexpr int V_CHUNK = BK * 128;  // 64 dims of a value block
+constexpr int V_BYTES = 2 * V_CHUNK;
+constexpr uint32_t TM_O = 256;  // S of group a at 128 a, O of group a at 256 + 128 a
+constexpr float kRescaleLog2 = 8.0f;
+constexpr int kSmemMax = 232448;  // 227 KB
 
-__global__ void __launch_bounds__(D)
-    tree_dims_kernel(const uint16_t* __restrict__ Q, int Hq, int Hkv, int T, int ldL, int k,
-                     const int32_t* __restrict__ lens, const int32_t* __restrict__ parents, int32_t* __restrict__ idx) {
+struct __align__(8) TreeBars {
+    uint64_t q_full, o_full, drain;
+    uint64_t k_full[kMaxStages], k_empty[kMaxStages];
+    uint64_t v_full[kMaxStages], v_empty[kMaxStages];
+    uint64_t s_full[2], p_full[2], pv_done[2];
+    uint64_t meet;  // all softmax warps
+    long long pos;  // the CTA's share: first block, and how many
+    int seg_b, seg_u, seg_blk, blocks;
+    uint32_t tmem_base;
+    int abort_flag;
+};
+
+struct TreeArgs {
+    const uint16_t* Q;
+    const int32_t *lens, *parents;
+    int32_t* idx;  // kept sets [B * Hkv * k]
+    uint16_t* O;
+    float* partials;
+    long long* cum;  // [B + 1]: blocks of the sequences before b
+    int* status;
+    int B, Hkv, G, T, ldL, R, nrt, nrp, k, kp, nk, nv, slot_rows;
+    int identity;    // every dim kept
+    float scale_log2;
+};
+
+__device__ __forceinline__ int blocks_of(const TreeArgs& a, int b) {
+    const int len = __ldg(a.lens + b);
+    return len < 0 || len > a.ldL - a.T ? 0 : (len + a.T + BK - 1) / BK;
+}
+
+// A CTA's share as its roles walk it, one piece of a unit at a time.
+struct Share {
+    int b, u, blk, left, n, nb;  // n: blocks of this piece, nb: of the whole unit
+    __device__ __forceinline__ bool next(const TreeArgs& a, const TreeBars* s, bool first) {
+        if (first) {
+            b = s->seg_b, u = s->seg_u, blk = s->seg_blk, left = s->blocks;
+            if (left <= 0) return false;
+            nb = blocks_of(a, b);
+        } else {
+            left -= n;
+            if (left <= 0) return false;
+            blk = 0;
+            if (++u == a.Hkv * a.nrp) {
+                u = 0;
+                do nb = blocks_of(a, ++b);
+                while (nb == 0);  // left > 0: a later sequence has blocks
+            }
+        }
+        n = min(nb - blk, left);
+        return true;
+    }
+};
+
+// floats of one partial: O in pieces of four dims [32][rows][4], then maxima, then sums
+__host__ __device__ constexpr size_t slot_floats(int rows) { return (size_t)rows * (D + 2); }
+
+// what the row of a node sees of the 32 keys from `key0` on, as a bit mask
+__device__ __forceinline__ uint32_t sees32(uint64_t way, int key0, int len) {
+    const int at = key0 - len;  // slot of the first of them in the tree
+    if (at <= -32) return way ? 0xFFFFFFFFu : 0u;
+    if (at >= 0) return at < 64 ? (uint32_t)(way >> at) : 0u;
+    return ((uint32_t)(way << -at)) | (way ? (1u << -at) - 1u : 0u);
+}
+
+__global__ void __launch_bounds__(kThreadsTree, 1)
+    attn_tree_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
+                     const __grid_constant__ CUtensorMap vmap, const TreeArgs a) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                               ~static_cast<uintptr_t>(1023));
+    const int QK_BYTES = a.kp * 256;  // a query tile or a key block
+    uint8_t* sV = smem;
+    uint8_t* sK = sV + a.nv * V_BYTES;
+    uint8_t* sQ = sK + a.nk * QK_BYTES;
+    TreeBars* bars = reinterpret_cast<TreeBars*>(sQ + (a.nrt > 1 ? 2 : 1) * QK_BYTES);
+    int32_t* par = reinterpret_cast<int32_t*>(bars + 1);
+    volatile int* abort_flag = &bars->abort_flag;
+    int* status = a.status;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+    if (tid == 0) {
+        mbar_init(smem_addr(&bars->q_full), a.identity ? 1 : kSoftmaxThreads);
+        mbar_init(smem_addr(&bars->o_full), 1);
+        mbar_init(smem_addr(&bars->drain), 1);
+        for (int s = 0; s < kMaxStages; ++s) {
+            mbar_init(smem_addr(&bars->k_full[s]), 1);
+            mbar_init(smem_addr(&bars->k_empty[s]), 1);
+            mbar_init(smem_addr(&bars->v_full[s]), 1);
+            mbar_init(smem_addr(&bars->v_empty[s]), 1);
+        }
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(smem_addr(&bars->s_full[s]), 1);
+            mbar_init(smem_addr(&bars->p_full[s]), 4);
+            mbar_init(smem_addr(&bars->pv_done[s]), 1);
+        }
+        mbar_init(smem_addr(&bars->meet), 8);
+        bars->abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == kMmaWarp) {
+        tmem_alloc(smem_addr(&bars->tmem_base), 512);
+        tmem_relinquish();
+    }
+    if (tid == 32 * kTmaWarp) {
+        tma_prefetch_desc(&kmap);
+        tma_prefetch_desc(&vmap);
+        tma_prefetch_desc(&qmap);
+    }
+    pdl_wait();  // lengths, trees, kept sets, queries and caches come from the preceding kernels
+    pdl_launch_dependents();
+    if (warp == 0) {
+        // the CTA's share of all blocks, and where it starts; the last CTA also leaves the
+        // running counts for the joining kernel
+        const int U = a.Hkv * a.nrp, c = blockIdx.x;
+        long long total = 0;
+        for (int b = lane; b < a.B; b += 32) {
+            total += blocks_of(a, b);
+            if (c == 0 && __ldg(a.lens + b) > a.ldL - a.T) record_status(status, RMM_ERR_INVALID_ARG);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+        total *= U;
+        // never more shares than blocks: no share between two others is empty
+        const long long C = min((long long)gridDim.x, total);
+        const long long p0 = c < C ? total * c / C : total, p1 = c < C ? total * (c + 1) / C : total;
+        long long base = 0;
+        for (int b0 = 0; b0 < a.B; b0 += 32) {
+            const int b = b0 + lane;
+            const long long n = b < a.B ? (long long)blocks_of(a, b) * U : 0;
+            long long end = n;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const long long v = __shfl_up_sync(0xffffffffu, end, o);
+                if (lane >= o) end += v;
+            }
+            end += base;
+            if (c == (int)gridDim.x - 1 && b < a.B) {
+                a.cum[b + 1] = end;
+                if (b == 0) a.cum[0] = 0;
+            }
+            if (p0 < end && p0 >= end - n) {  // one lane of one round
+                const int nb = (int)(n / U);
+                const long long in = p0 - (end - n);
+                bars->seg_b = b;
+                bars->seg_u = (int)(in / nb);
+                bars->seg_blk = (int)(in % nb);
+            }
+            base = __shfl_sync(0xffffffffu, end, 31);
+        }
+        if (lane == 0) bars->blocks = (int)(p1 - p0);
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = bars->tmem_base;
+
+    Share w;
+    if (warp == kTmaWarp) {
+        // ------------------------------------------------------------ key and value blocks
+        int c = 0;  // blocks issued
+        bool ok = true;
+        const int oob = a.B * a.Hkv * D;  // a row outside the key map: reads as zeros
+        for (bool more = w.next(a, bars, true); ok && more; more = w.next(a, bars, false)) {
+            const int plane = w.b * a.Hkv + w.u / a.nrp;
+            int r0 = 0, r1 = 0, r2 = 0, r3 = 0;
+            if (!a.identity && lane * 4 < a.kp) {  // this lane's four kept rows of K^T
+                const int32_t* S = a.idx + (size_t)plane * a.k + lane * 4;
+                r0 = lane * 4 + 0 < a.k ? plane * D + S[0] : oob;
+                r1 = lane * 4 + 1 < a.k ? plane * D + S[1] : oob;
+                r2 = lane * 4 + 2 < a.k ? plane * D + S[2] : oob;
+                r3 = lane * 4 + 3 < a.k ? plane * D + S[3] : oob;
+            }
+            for (int j = 0; j < w.n; ++j, ++c) {
+                const int key0 = (w.blk + j) * BK;
+                const int ks = c % a.nk, vs = c % a.nv;
+                if (!__all_sync(0xffffffffu, mbar_wait(smem_addr(&bars->k_empty[ks]), ((uint32_t)(c / a.nk) & 1u) ^ 1u,
+                                                       status, abort_flag))) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t kb = smem_addr(sK + ks * QK_BYTES), kf = smem_addr(&bars->k_full[ks]);
+                if (lane == 0) mbar_arrive_expect_tx(kf, QK_BYTES);
+                __syncwarp();
+                if (a.identity) {
+                    if (lane == 0) {
+                        tma_load_3d(kb, &kmap, kf, key0, 0, plane);
+                        tma_load_3d(kb + D * 128, &kmap, kf, key0 + 64, 0, plane);
+                    }
+                } else if (lane * 4 < a.kp) {
+                    tma_gather4(kb + lane * 512, &kmap, kf, key0, r0, r1, r2, r3);
+                    tma_gather4(kb + a.kp * 128 + lane * 512, &kmap, kf, key0 + 64, r0, r1, r2, r3);
+                }
+                const bool got = mbar_wait(smem_addr(&bars->v_empty[vs]), ((uint32_t)(c / a.nv) & 1u) ^ 1u, status,
+                                           abort_flag);
+                if (!__all_sync(0xffffffffu, got)) {
+                    // this block's keys are on their way, its values are not
+                    if (lane == 0) {
+                        volatile int no_abort = 0;
+                        mbar_wait(kf, (uint32_t)(c / a.nk) & 1u, status, &no_abort);
+                    }
+                    ok = false;
+                    break;
+                }
+                if (lane == 0) {
+                    const uint32_t vb = smem_addr(sV + vs * V_BYTES), vf = smem_addr(&bars->v_full[vs]);
+                    mbar_arrive_expect_tx(vf, V_BYTES);
+                    tma_load_3d(vb, &vmap, vf, 0, key0, plane);
+                    tma_load_3d(vb + V_CHUNK, &vmap, vf, 64, key0, plane);
+                }
+                __syncwarp();
+            }
+        }
+        // no copy may still be landing when the CTA leaves (after an abort; else all were consumed)
+        if (lane == 0) {
+            volatile int no_abort = 0;
+            for (int j = max(0, c - a.nk); j < c; ++j)
+                mbar_wait(smem_addr(&bars->k_full[j % a.nk]), (uint32_t)(j / a.nk) & 1u, status, &no_abort);
+            for (int j = max(0, c - a.nv); j < c; ++j)
+                mbar_wait(smem_addr(&bars->v_full[j % a.nv]), (uint32_t)(j / a.nv) & 1u, status, &no_abort);
+        }
+        __syncwarp();
+    } else if (warp == kMmaWarp) {
+        // ------------------------------------------------------------ MMA issuer
+        const uint32_t idesc_s = idesc_bf16_f32(BM, BK, a.identity ? 0 : 1, 1);
+        const uint32_t idesc_pv = idesc_bf16_f32(BM, D, 0, 1);
+        int kc0 = 0;           // blocks of the pieces before
+        int pc[2] = {0, 0};    // P.V products issued per group
+        int piece = 0;
+        bool ok = true;
+        for (bool more = w.next(a, bars, true); ok && more; more = w.next(a, bars, false), ++piece) {
+            const int rp = w.u % a.nrp;
+            const bool two = 2 * rp + 1 < a.nrt;
+            const int steps = two ? 2 * w.n : w.n;
+            const int len = __ldg(a.lens + w.b);
+            ok = __all_sync(0xffffffffu, mbar_wait(smem_addr(&bars->q_full), (uint32_t)piece & 1u, status, abort_flag));
+            auto issue_s = [&](int s) -> bool {
+                const int g = s & 1, c = kc0 + (two ? s >> 1 : s), ks = c % a.nk;
+                bool got = mbar_wait(smem_addr(&bars->k_full[ks]), (uint32_t)(c / a.nk) & 1u, status, abort_flag);
+                // P.V of the group's step before has read P, which lies over S
+                if (pc[g] > 0)
+                    got = got && mbar_wait(smem_addr(&bars->pv_done[g]), (uint32_t)(pc[g] - 1) & 1u, status, abort_flag);
+                if (!__all_sync(0xffffffffu, got)) return false;
+                tc_fence_after();
+                if (lane == 0) {
+                    const uint32_t qb = smem_addr(sQ + (two ? g : 0) * QK_BYTES), kb = smem_addr(sK + ks * QK_BYTES);
+                    for (int kk = 0; kk < a.kp / 16; ++kk) {
+                        const uint64_t qd = a.identity
+                                                ? smem_desc_sw128(qb + (kk >> 2) * (BM * 128) + (kk & 3) * 32, 16, 1024)
+                                                : smem_desc_sw128(qb + kk * 2048, a.kp * 128, 1024);
+                        umma_f16(tmem + g * BK, qd, smem_desc_sw128(kb + kk * 2048, a.kp * 128, 1024), idesc_s,
+                                 kk > 0 ? 1u : 0u);
+                    }
+                    umma_commit(smem_addr(&bars->s_full[g]));
+                    if (!two || g == 1) umma_commit(smem_addr(&bars->k_empty[ks]));
+                }
+                __syncwarp();
+                return true;
+            };
+            if (ok) {
+                fence_proxy_async_smem();  // a gathered query operand, written by the softmax warps
+                tc_fence_after();
+                ok = issue_s(0);
+            }
+            if (ok && steps > 1) ok = issue_s(1);
+            for (int s = 0; ok && s < steps; ++s) {
+                const int g = s & 1, j = two ? s >> 1 : s, c = kc0 + j, vs = c % a.nv;
+                const bool got = mbar_wait(smem_addr(&bars->v_full[vs]), (uint32_t)(c / a.nv) & 1u, status, abort_flag) &&
+                                 mbar_wait(smem_addr(&bars->p_full[g]), (uint32_t)pc[g] & 1u, status, abort_flag);
+                if (!__all_sync(0xffffffffu, got)) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t vb = smem_addr(sV + vs * V_BYTES);
+                const int at = (w.blk + j) * BK - len;  // the block's first key as a slot of the tree
+                if (at + BK > 0 && (!two || g == 0)) {
+                    // slots that no node holds may contain anything: their values become zeros
+                    uint64_t there = ~0ull >> (kTreeMax - a.T);
+                    if (a.parents) {
+                        const uint32_t lo = __ballot_sync(0xffffffffu, lane < a.T && tree_way(par, lane) != 0);
+                        const uint32_t hi = __ballot_sync(0xffffffffu, lane + 32 < a.T && tree_way(par, lane + 32) != 0);
+                        there = (uint64_t)lo | ((uint64_t)hi << 32);
+                    }
+                    for (int i = lane; i < BK * 8; i += 32) {
+                        const int slot = at + (i >> 3);
+                        if (slot >= 0 && (slot >= a.T || !((there >> slot) & 1))) {
+                            st_shared_v4(vb + i * 16, make_uint4(0, 0, 0, 0));
+                            st_shared_v4(vb + V_CHUNK + i * 16, make_uint4(0, 0, 0, 0));
+                        }
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                }
+                tc_fence_after();
+                if (lane == 0) {
+                    const bool fresh = two ? j == 0 : s < 2;  // the group's first block of the piece
+#pragma unroll
+                    for (int kk = 0; kk < BK / 16; ++kk)
+                        umma_f16_tmem_a(tmem + TM_O + g * D, tmem + g * BK + kk * 8,
+                                        smem_desc_sw128(vb + kk * 2048, V_CHUNK, 1024), idesc_pv,
+                                        fresh && kk == 0 ? 0u : 1u);
+                    umma_commit(smem_addr(&bars->pv_done[g]));
+                    if (!two || g == 1) umma_commit(smem_addr(&bars->v_empty[vs]));
+                }
+                __syncwarp();
+                ++pc[g];
+                if (s + 2 < steps) ok = issue_s(s + 2);
+            }
+            if (ok && lane == 0) umma_commit(smem_addr(&bars->o_full));
+            __syncwarp();
+            kc0 += w.n;
+        }
+        if (lane == 0) umma_commit(smem_addr(&bars->drain));
+        __syncwarp();
+        // issued MMAs finish on their own; TMEM is not freed under them
+        volatile int no_abort = 0;
+        mbar_wait(smem_addr(&bars->drain), 0, status, &no_abort);
+    } else {
+        // ------------------------------------------------------------ softmax, query operand, output
+        const int grp = warp >> 2, i = tid & 127;  // group, row of the tile = TMEM lane
+        const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t s_col = tmem + lane_base + grp * BK, meet = smem_addr(&bars->meet);
+        float* xch = reinterpret_cast<float*>(sQ);  // maxima and sums of the two groups (sQ is free by then)
+        int steps_done = 0, piece = 0, meets = 0, queries = 0;
+        // all softmax warps meet (bounded)
+        auto together = [&]() -> bool {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(meet);
+            return __all_sync(0xffffffffu, mbar_wait(meet, (uint32_t)(meets++) & 1u, status, abort_flag));
+        };
+        bool ok = true;
+        for (bool more = w.next(a, bars, true); ok && more; more = w.next(a, bars, false), ++piece) {
+            const int g = w.u / a.nrp, rp = w.u % a.nrp;
+            const bool two = 2 * rp + 1 < a.nrt;
+            const int plane = w.b * a.Hkv + g;
+            const int len = __ldg(a.lens + w.b);
+            const int tile = 2 * rp + (two ? grp : 0);
+            const int row = tile * BM + i;  // of the unit's G * T rows: query head row / T, node row % T
+            const size_t row0 = (size_t)plane * a.R;
+            // the tree and the query operand; the piece before is done with both (and with the
+            // maxima and sums that lay where a copy now writes)
+            fence_proxy_async_smem();
+            if (!together()) break;
+            if (a.parents && tid < a.T) par[tid] = __ldg(a.parents + (size_t)w.b * a.T + tid);
+            if (a.identity) {
+                if (tid == 0) {
+                    const uint32_t qf = smem_addr(&bars->q_full), qb = smem_addr(sQ);
+                    mbar_arrive_expect_tx(qf, (two ? 2 : 1) * BM * 256);
+                    for (int t = 0; t < (two ? 2 : 1); ++t)
+                        for (int h = 0; h < 2; ++h)
+                            tma_load_2d(qb + t * QK_BYTES + h * BM * 128, &qmap, qf, h * 64,
+                                        (int)(row0 + (2 * rp + t) * BM));
+                }
+                ++queries;
+                if (w.blk == 0 && rp == 0 && a.idx && tid < D) a.idx[(size_t)plane * D + tid] = tid;
+            } else {
+                // the kept dims of 8 rows at a time; both groups share the work of one tile
+                const int32_t* S = a.idx + (size_t)plane * a.k;
+                const int tiles = two ? 2 : 1;
+                for (int it = tid; it < a.kp * 16 * tiles; it += kSoftmaxThreads) {
+                    const int jr = it % a.kp, c16 = (it / a.kp) & 15, t = it / (a.kp * 16);
+                    const int dim = jr < a.k ? __ldg(S + jr) : -1;
+                    const int r = (2 * rp + t) * BM + c16 * 8;
+                    uint16_t v[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        v[e] = dim >= 0 && r + e < a.R ? a.Q[(row0 + r + e) * D + dim] : (uint16_t)0;
+                    st_shared_v4(smem_addr(sQ + t * QK_BYTES) + swz(jr, c16, a.kp * 128),
+                                 make_uint4(v[0] | ((uint32_t)v[1] << 16), v[2] | ((uint32_t)v[3] << 16),
+                                            v[4] | ((uint32_t)v[5] << 16), v[6] | ((uint32_t)v[7] << 16)));
+                }
+                fence_proxy_async_smem();
+                mbar_arrive(smem_addr(&bars->q_full));
+            }
+            if (!together()) break;  // par
+            uint64_t way = 0;
+            if (row < a.R) way = a.parents ? tree_way(par, row % a.T) : chain_way(row % a.T);
+            const bool busy = __any_sync(0xffffffffu, row < a.R);  // the warp has rows
+
+            const int mine = two ? w.n : (w.n + 1 - grp) / 2;  // this group's steps
+            float m_use = -INFINITY, l = 0.0f;
+            for (int s = 0; s < mine; ++s, ++steps_done) {
+                if (!__all_sync(0xffffffffu, mbar_wait(smem_addr(&bars->s_full[grp]), (uint32_t)steps_done & 1u, status,
+                                                       abort_flag))) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                if (busy) {
+                    const int key0 = (w.blk + (two ? s : 2 * s + grp)) * BK;
+                    uint32_t x[4][32];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) tmem_ld_32x32b_x32(s_col + q * 32, x[q]);
+                    tmem_ld_wait();
+                    if (key0 + BK > len) {  // the block reaches the tree's slots
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            const uint32_t see = sees32(way, key0 + q * 32, len);
+#pragma unroll
+                            for (int c = 0; c < 32; ++c)
+                                if (!((see >> c) & 1u)) x[q][c] = 0xFF800000u;  // -inf
+                        }
+                    }
+                    float mx[4];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        mx[q] = __uint_as_float(x[q][0]);
+#pragma unroll
+                        for (int c = 1; c < 32; ++c) mx[q] = fmaxf(mx[q], __uint_as_float(x[q][c]));
+                    }
+                    const float m_blk = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2;
+                    const bool resc = m_blk > m_use + kRescaleLog2;
+                    const float m_new = resc ? m_blk : m_use;
+                    const float alpha = resc ? exp2f(m_use - m_new) : 1.0f;
+                    const float neg_m = m_new == -INFINITY ? 0.0f : -m_new;
+                    if (s > 0 && __any_sync(0xffffffffu, resc)) {
+                        // the group's P.V so far are done (S of this step was issued after them)
+#pragma unroll 1
+                        for (int q = 0; q < 4; ++q) {
+                            uint32_t o[32];
+                            const uint32_t oc = tmem + lane_base + TM_O + grp * D + q * 32;
+                            tmem_ld_32x32b_x32(oc, o);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * alpha);
+                            tmem_st_32x32b_x32(oc, o);
+                        }
+                    }
+                    m_use = m_new;
+                    float sm[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        uint32_t pk[16];
+#pragma unroll
+                        for (int c = 0; c < 32; c += 2) {
+                            const float y0 = fmaf(__uint_as_float(x[q][c]), a.scale_log2, neg_m);
+                            const float y1 = fmaf(__uint_as_float(x[q][c + 1]), a.scale_log2, neg_m);
+                            const float p0 = fast_exp2(y0);
+                            // the polynomial ends at 2^-126, which P rounds to no weight next to a
+                            // row's largest; a masked key's weight is exactly 0
+                            const float p1 = y1 < -126.0f ? 0.0f : poly_exp2(y1);
+                            sm[(c >> 1) & 3] += p0 + p1;
+                            pk[c >> 1] = pack_bf16x2(p0, p1);
+                        }
+                        tmem_st_32x32b_x16(s_col + q * 16, pk);  // P over columns of S that are already read
+                    }
+                    tmem_st_wait();
+                    l = l * alpha + ((sm[0] + sm[1]) + (sm[2] + sm[3]));
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_addr(&bars->p_full[grp]));
+            }
+            if (!ok) break;
+            if (!__all_sync(0xffffffffu,
+                            mbar_wait(smem_addr(&bars->o_full), (uint32_t)piece & 1u, status, abort_flag))) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            if (way == 0) m_use = -INFINITY, l = 0.0f;  // an absent node sees nothing
+            const bool whole = w.n == w.nb;
+            float* slot = a.partials + (size_t)(2 * blockIdx.x + (w.left == bars->blocks ? 0 : 1)) * slot_floats(a.slot_rows);
+            if (two) {
+                const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+                const int sr = grp * BM + i;
+                if (!whole && row < a.R) {
+                    slot[D * a.slot_rows + sr] = m_use;
+                    slot[(D + 1) * a.slot_rows + sr] = l;
+                }
+#pragma unroll 1
+                for (int q = 0; q < 4; ++q) {
+                    uint32_t o[32];
+                    __syncwarp();
+                    tmem_ld_32x32b_x32(tmem + lane_base + TM_O + grp * D + q * 32, o);
+                    tmem_ld_wait();
+                    if (row >= a.R) continue;
+                    if (whole) {
+                        uint4* dst = reinterpret_cast<uint4*>(a.O + (row0 + row) * D + q * 32);
+#pragma unroll
+                        for (int v = 0; v < 4; ++v) {
+                            float f[8];
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) f[e] = l > 0.0f ? __uint_as_float(o[v * 8 + e]) * inv : 0.0f;
+                            dst[v] = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]),
+                                                pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
+                        }
+                    } else {
+#pragma unroll
+                        for (int v = 0; v < 8; ++v)
+                            *reinterpret_cast<uint4*>(slot + ((size_t)(q * 8 + v) * a.slot_rows + sr) * 4) =
+                                make_uint4(o[v * 4], o[v * 4 + 1], o[v * 4 + 2], o[v * 4 + 3]);
+                    }
+                }
+            } else {
+                // both groups hold a part of the same rows: join them, 64 dims each
+                xch[grp * BM + i] = m_use;
+                xch[2 * BM + grp * BM + i] = l;
+                tc_fence_before();
+                if (!together()) break;
+                tc_fence_after();
+                const float m0 = xch[i], m1 = xch[BM + i], l0 = xch[2 * BM + i], l1 = xch[3 * BM + i];
+                const float M = fmaxf(m0, m1);
+                const float w0 = m0 == -INFINITY ? 0.0f : exp2f(m0 - M), w1 = m1 == -INFINITY ? 0.0f : exp2f(m1 - M);
+                const float L = w0 * l0 + w1 * l1;
+                const float inv = whole ? (L > 0.0f ? 1.0f / L : 0.0f) : 1.0f;
+                const bool second = w.n > 1;  // group 1 had a step: O1 holds this unit's data
+                if (!whole && row < a.R && grp == 0) {
+                    slot[D * a.slot_rows + i] = M;
+                    slot[(D + 1) * a.slot_rows + i] = L;
+                }
+#pragma unroll 1
+                for (int q = 0; q < 2 && busy; ++q) {
+                    uint32_t o0[32], o1[32];
+                    const uint32_t oc = tmem + lane_base + TM_O + grp * 64 + q * 32;
+                    __syncwarp();
+                    tmem_ld_32x32b_x32(oc, o0);
+                    if (second) tmem_ld_32x32b_x32(oc + D, o1);
+                    tmem_ld_wait();
+                    if (row >= a.R) continue;
+                    float f[32];
+#pragma unroll
+                    for (int c = 0; c < 32; ++c) {
+                        // an output that no key went into (weight 0) may hold anything
+                        const float u0 = w0 > 0.0f ? __uint_as_float(o0[c]) * w0 : 0.0f;
+                        const float u1 = second && w1 > 0.0f ? __uint_as_float(o1[c]) * w1 : 0.0f;
+                        f[c] = (u0 + u1) * inv;
+                    }
+                    if (whole) {
+                        uint4* dst = reinterpret_cast<uint4*>(a.O + (row0 + row) * D + grp * 64 + q * 32);
+#pragma unroll
+                        for (int v = 0; v < 4; ++v)
+                            dst[v] = make_uint4(pack_bf16x2(f[v * 8], f[v * 8 + 1]), pack_bf16x2(f[v * 8 + 2], f[v * 8 + 3]),
+                                                pack_bf16x2(f[v * 8 + 4], f[v * 8 + 5]), pack_bf16x2(f[v * 8 + 6], f[v * 8 + 7]));
+                    } else {
+#pragma unroll
+                        for (int v = 0; v < 8; ++v)
+                            *reinterpret_cast<float4*>(slot + ((size_t)(grp * 16 + q * 8 + v) * a.slot_rows + i) * 4) =
+                                make_float4(f[v * 4], f[v * 4 + 1], f[v * 4 + 2], f[v * 4 + 3]);
+                    }
+                }
+            }
+            tc_fence_before();
+        }
+        // no query copy may still be landing when the CTA leaves (after an abort)
+        if (tid == 0 && queries > 0) {
+            volatile int no_abort = 0;
+            mbar_wait(smem_addr(&bars->q_full), (uint32_t)(queries - 1) & 1u, status, &no_abort);
+        }
+        __syncwarp();
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
+}
+
+// The partials of a unit that was cut, joined: thread (row, four dims).  Also the
+// zeros of empty slots.  Memory bound on what the cuts left in L2.
+__global__ void __launch_bounds__(256) attn_tree_join_kernel(const TreeArgs a, int ctas) {
+    const int U = a.Hkv * a.nrp;
+    pdl_wait();
+    pdl_launch_dependents();
+    const int unit = blockIdx.x, b = unit / U, u = unit % U, g = u / a.nrp, rp = u % a.nrp;
+    const int rows = min(2 * BM, a.R - rp * 2 * BM);
+    const long long lo = a.cum[b], nb = (a.cum[b + 1] - lo) / U, total = a.cum[a.B];
+    const long long C = min((long long)ctas, total);
+    const size_t row0 = ((size_t)b * a.Hkv + g) * a.R + rp * 2 * BM;
+    const long long p0 = lo + u * nb, p1 = p0 + nb;  // the unit's blocks
+    // share c is [total c / C, total (c + 1) / C): the shares of its first and last block
+    const int c0 = nb ? (int)(((p0 + 1) * C - 1) / total) : 0, c1 = nb ? (int)((p1 * C - 1) / total) : 0;
+    if (nb && c0 == c1) return;
+    for (int it = blockIdx.y * 256 + threadIdx.x; it < rows * 32; it += gridDim.y * 256) {
+        const int r = it % rows, c4 = it / rows;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (nb) {
+            const size_t sf = slot_floats(a.slot_rows);
+            // the first share may have begun with another unit: its piece is then its second
+            const float* first = a.partials + (size_t)(2 * c0 + (total * c0 / C < p0 ? 1 : 0)) * sf;
+            float M = -INFINITY;
+            for (int c = c0; c <= c1; ++c)
+                M = fmaxf(M, (c == c0 ? first : a.partials + (size_t)2 * c * sf)[D * a.slot_rows + r]);
+            float L = 0.f;
+            if (M > -INFINITY) {
+#pragma unroll 4
+                for (int c = c0; c <= c1; ++c) {
+                    const float* s = c == c0 ? first : a.partials + (size_t)2 * c * sf;
+                    const float w = exp2f(s[D * a.slot_rows + r] - M);
+                    const float4 v = *reinterpret_cast<const float4*>(s + ((size_t)c4 * a.slot_rows + r) * 4);
+                    if (w > 0.f) {
+                        L = fmaf(w, s[(D + 1) * a.slot_rows + r], L);
+                        o.x = fmaf(w, v.x, o.x);
+                        o.y = fmaf(w, v.y, o.y);
+                        o.z = fmaf(w, v.z, o.z);
+                        o.w = fmaf(w, v.w, o.w);
+                    }
+                }
+            }
+            const float inv = L > 0.f ? 1.0f / L : 0.f;
+            o = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+        }
+        *reinterpret_cast<uint2*>(a.O + (row0 + r) * D + c4 * 4) =
+            make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
+    }
+}
+
+// The kept dims of one (sequence, KV head): the column maximum of |Q| over the
+// present rows, 16 row lanes x 16 pieces of 8 dims, then the exact rank of each
+// dim under (score desc, index asc).
+__global__ void __launch_bounds__(256) tree_dims_kernel(const TreeArgs a) {
     __shared__ int32_t par[kTreeMax];
+    __shared__ uint64_t there_s;
+    __shared__ uint32_t red[16][D];
     __shared__ uint32_t sv[D];
     __shared__ int warp_cnt[D / 32];
-    const int b = blockIdx.x / Hkv, g = blockIdx.x % Hkv, G = Hq / Hkv, j = threadIdx.x;
+    const int plane = blockIdx.x, b = plane / a.Hkv, tid = threadIdx.x;
     pdl_wait();
     pdl_launch_dependents();
-    if (lens[b] < 0 || lens[b] > ldL - T) return;
-    if (parents && j < T) par[j] = parents[(size_t)b * T + j];
-    __syncthreads();
-    uint32_t m = 0;
-    for (int t = 0; t < T; ++t) {
-        if (parents && tree_way(par, t) == 0) continue;
-        for (int q = 0; q < G; ++q) m = max(m, (uint32_t)(Q[(((size_t)b * Hq + g * G + q) * T + t) * D + j] & 0x7FFF));
+    if (blocks_of(a, b) == 0) return;
+    uint64_t there = ~0ull;
+    if (a.parents) {
+        if (tid == 0) there_s = 0;
+        if (tid < a.T) par[tid] = __ldg(a.parents + (size_t)b * a.T + tid);
+        __syncthreads();
+        if (tid < a.T && tree_way(par, tid))
+            atomicOr(reinterpret_cast<unsigned long long*>(&there_s), 1ull << tid);
+        __syncthreads();
+        there = there_s;
     }
-    sv[j] = m;
+    const int c16 = tid & 15, rl = tid >> 4;
+    uint32_t m[4] = {0, 0, 0, 0};  // two dims each, magnitudes of 15 bits
+    const uint16_t* q = a.Q + (size_t)plane * a.R * D + c16 * 8;
+#pragma unroll 4
+    for (int r = rl; r < a.R; r += 16) {
+        if (!((there >> (r % a.T)) & 1)) continue;
+        const uint4 v = ld_nc_v4(q + (size_t)r * D);
+        m[0] = __vmaxu2(m[0], v.x & 0x7FFF7FFFu);
+        m[1] = __vmaxu2(m[1], v.y & 0x7FFF7FFFu);
+        m[2] = __vmaxu2(m[2], v.z & 0x7FFF7FFFu);
+        m[3] = __vmaxu2(m[3], v.w & 0x7FFF7FFFu);
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        red[rl][c16 * 8 + 2 * e] = m[e] & 0xFFFFu;
+        red[rl][c16 * 8 + 2 * e + 1] = m[e] >> 16;
+    }
     __syncthreads();
-    int rank = 0;
-    for (int i = 0; i < D; ++i) rank += sv[i] > m || (sv[i] == m && i < j);
-    const bool keep = rank < k;
+    uint32_t s = 0;
+    if (tid < D) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) s = max(s, red[i][tid]);
+        sv[tid] = s;
+    }
+    __syncthreads();
+    bool keep = false;
+    if (tid < D) {
+        int rank = 0;
+#pragma unroll 16
+        for (int i = 0; i < D; ++i) rank += sv[i] > s || (sv[i] == s && i < tid);
+        keep = rank < a.k;
+    }
     const unsigned ball = __ballot_sync(0xffffffffu, keep);
-    if ((j & 31) == 0) warp_cnt[j >> 5] = __popc(ball);
+    if (tid < D && (tid & 31) == 0) warp_cnt[tid >> 5] = __popc(ball);
     __syncthreads();
-    int pos = __popc(ball & ((1u << (j & 31)) - 1u));
-    for (int i = 0; i < (j >> 5); ++i) pos += warp_cnt[i];
-    if (keep) idx[(size_t)blockIdx.x * k + pos] = j;
+    if (keep) {
+        int pos = __popc(ball & ((1u << (tid & 31)) - 1u));
+        for (int i = 0; i < (tid >> 5); ++i) pos += warp_cnt[i];
+        a.idx[(size_t)plane * a.k + pos] = tid;
+    }
 }
 
-__global__ void __launch_bounds__(D)
-    attn_tree_kernel(const uint16_t* __restrict__ Q, const uint16_t* __restrict__ Kt, const uint16_t* __restrict__ V,
-                     int Hq, int Hkv, int T, int ldL, int k, float scale, const int32_t* __restrict__ lens,
-                     const int32_t* __restrict__ parents, const int32_t* __restrict__ idx, uint16_t* __restrict__ O,
-                     int* status) {
-    __shared__ int32_t par[kTreeMax];
-    __shared__ float qs[D], p_s[D];
-    __shared__ int sidx[D];
-    __shared__ float red[4];
-    const int t = blockIdx.x, h = blockIdx.y, b = blockIdx.z, tid = threadIdx.x;
-    const int g = h / (Hq / Hkv);
-    pdl_wait();
-    pdl_launch_dependents();
-    const size_t row = ((size_t)b * Hq + h) * T + t;
-    const int len = lens[b];
-    if (len > ldL - T && t == 0 && h == 0 && tid == 0) record_status(status, RMM_ERR_INVALID_ARG);
-    if (parents && tid < T) par[tid] = parents[(size_t)b * T + tid];
-    __syncthreads();
-    const uint64_t way = len < 0 || len > ldL - T ? 0 : parents ? tree_way(par, t) : chain_way(t);
-    float acc = 0.f, m = -INFINITY, l = 0.f;
-    if (way) {
-        if (tid < k) {
-            sidx[tid] = idx[((size_t)b * Hkv + g) * k + tid];
-            qs[tid] = bf16_bits_to_float(Q[row * D + sidx[tid]]) * scale;
-        }
-        __syncthreads();
-        const uint16_t* Kg = Kt + ((size_t)b * Hkv + g) * D * (size_t)ldL;
-        const uint16_t* Vg = V + ((size_t)b * Hkv + g) * (size_t)ldL * D;
-        for (int l0 = 0; l0 < len + T; l0 += D) {
-            const int key = l0 + tid;
-            float x = -INFINITY;
-            if (key < len || (key < len + T && ((way >> (key - len)) & 1))) {
-                x = 0.f;
-                for (int j = 0; j < k; ++j) x = fmaf(qs[j], bf16_bits_to_float(Kg[(size_t)sidx[j] * ldL + key]), x);
-            }
-            float mx = x;
-            for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-            if ((tid & 31) == 0) red[tid >> 5] = mx;
-            __syncthreads();
-            const float m_new = fmaxf(m, fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3])));
-            const float p = x == -INFINITY ? 0.f : expf(x - m_new);
-            const float alpha = m == -INFINITY ? 0.f : expf(m - m_new);
-            p_s[tid] = p;
-            __syncthreads();
-            acc *= alpha;
-            l *= alpha;
-            m = m_new;
-            const int n = min(D, len + T - l0);
-            for (int i = 0; i < n; ++i) {
-                if (p_s[i] == 0.f) continue;
-                l += p_s[i];
-                acc = fmaf(p_s[i], bf16_bits_to_float(Vg[(size_t)(l0 + i) * D + tid]), acc);
-            }
-            __syncthreads();
-        }
-    }
-    O[row * D + tid] = float_to_bf16_bits(l > 0.f ? acc / l : 0.f);
+struct TreePlan {
+    int R, nrt, nrp, slot_rows, ctas;
+};
+
+TreePlan tree_plan(int B, int Hq, int Hkv, int T, int ldL, int num_sms) {
+    TreePlan p;
+    p.R = Hq / Hkv * T;
+    p.nrt = (p.R + BM - 1) / BM;
+    p.nrp = (p.nrt + 1) / 2;
+    p.slot_rows = p.R < 2 * BM ? (p.R + 3) / 4 * 4 : 2 * BM;
+    const long long most = (long long)B * Hkv * p.nrp * ((ldL + BK - 1) / BK);
+    p.ctas = most < num_sms ? (int)most : num_sms;
+    return p;
 }
+
+size_t cum_bytes(int B) { return ((size_t)(B + 1) * sizeof(long long) + 255) / 256 * 256; }
 
 }  // namespace
 
-size_t attn_tree_partial_bytes(int, int, int, int, int, int) { return 0; }
+size_t attn_tree_partial_bytes(int B, int Hq, int Hkv, int T, int ldL, int num_sms) {
+    const TreePlan p = tree_plan(B, Hq, Hkv, T, ldL, num_sms);
+    return cum_bytes(B) + (size_t)p.ctas * 2 * slot_floats(p.slot_rows) * sizeof(float);
+}
 
-cudaError_t launch_attn_tree(const uint16_t* Q, const uint16_t* Kt, const uint16_t* V, int B, int Hq, int Hkv, int T,
-                             int ldL, int k, float scale, const int32_t* lens, const int32_t* parents, uint16_t* O,
-                             int32_t* idx, float* partials, int* status, int num_sms, cudaStream_t stream) {
-    cudaError_t e = launch_pdl(tree_dims_kernel, dim3(B * Hkv), dim3(D), 0, stream, Q, Hq, Hkv, T, ldL, k, lens,
-                               parents, idx);
+cudaError_t launch_attn_tree(const CUtensorMap& qmap, const CUtensorMap& kmap, const CUtensorMap& vmap,
+                             const uint16_t* Q, int B, int Hq, int Hkv, int T, int ldL, int k, float scale,
+                             const int32_t* lens, const int32_t* parents, uint16_t* O, int32_t* idx, int want_idx,
+                             void* partials, int* status, int num_sms, cudaStream_t stream) {
+    const TreePlan p = tree_plan(B, Hq, Hkv, T, ldL, num_sms);
+    TreeArgs a{};
+    a.Q = Q;
+    a.lens = lens;
+    a.parents = parents;
+    a.identity = k == D;
+    a.idx = a.identity && !want_idx ? nullptr : idx;
+    a.O = O;
+    a.cum = static_cast<long long*>(partials);
+    a.partials = reinterpret_cast<float*>(static_cast<uint8_t*>(partials) + cum_bytes(B));
+    a.status = status;
+    a.B = B, a.Hkv = Hkv, a.G = Hq / Hkv, a.T = T, a.ldL = ldL;
+    a.R = p.R, a.nrt = p.nrt, a.nrp = p.nrp, a.slot_rows = p.slot_rows;
+    a.k = k;
+    a.kp = (k + 15) / 16 * 16;
+    a.scale_log2 = scale * 1.4426950408889634f;
+    // rings: two stages each, then more values and keys by turns while they fit
+    const int qk = a.kp * 256;
+    const int fixed = 1024 + (p.nrt > 1 ? 2 : 1) * qk + (int)sizeof(TreeBars) + kTreeMax * 4;
+    a.nk = a.nv = 2;
+    for (bool grew = true; grew;) {
+        grew = false;
+        if (a.nv < kMaxStages && fixed + (a.nv + 1) * V_BYTES + a.nk * qk <= kSmemMax) ++a.nv, grew = true;
+        if (a.nk < kMaxStages && a.nk < a.nv && fixed + a.nv * V_BYTES + (a.nk + 1) * qk <= kSmemMax) ++a.nk, grew = true;
+    }
+    const size_t smem = fixed + (size_t)a.nv * V_BYTES + (size_t)a.nk * qk;
+    cudaError_t e = ensure_smem_limit(attn_tree_kernel, smem);
     if (e != cudaSuccess) return e;
-    return launch_pdl(attn_tree_kernel, dim3(T, Hq, B), dim3(D), 0, stream, Q, Kt, V, Hq, Hkv, T, ldL, k, scale, lens,
-                      parents, (const int32_t*)idx, O, status);
+    if (!a.identity) {
+        e = launch_pdl(tree_dims_kernel, dim3(B * Hkv), dim3(256), 0, stream, a);
+        if (e != cudaSuccess) return e;
+    }
+    e = launch_pdl(attn_tree_kernel, dim3(p.ctas), dim3(kThreadsTree), smem, stream, qmap, kmap, vmap, a);
+    if (e != cudaSuccess) return e;
+    const int most_rows = p.R < 2 * BM ? p.R : 2 * BM;
+    return launch_pdl(attn_tree_join_kernel, dim3(B * Hkv * p.nrp, (most_rows * 32 + 255) / 256), dim3(256), 0, stream, a,
+                      p.ctas);
 }
 
 }  // namespace rmm

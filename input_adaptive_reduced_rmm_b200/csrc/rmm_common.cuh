@@ -484,6 +484,42 @@ __host__ __device__ constexpr uint32_t idesc_bf16_f32_mn_mn(int M, int N) {
            | ((uint32_t)(M >> 4) << 24);  // M / 16
 }
 
+// ---------------------------------------------------------------- tensor-core attention
+
+// 2^x with the hardware approximation (ex2.approx.ftz: ~2 ulp; -inf gives 0);
+// P is rounded to bf16 right after, so its error is far below that rounding.
+__device__ __forceinline__ float fast_exp2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// 2^x on the FMA pipe, for x <= 8 (P's range): round-to-nearest range
+// reduction x = n + f, |f| <= 1/2, by adding 1.5 * 2^23 (the integer n lands
+// in the low mantissa bits); 2^f = e^(f ln 2) by its Taylor expansion to
+// degree 4 (remainder < 6e-5 relative for |f ln 2| <= 0.35, well below the
+// bf16 rounding of P); n is added to the exponent bits.  x below -126 is
+// clamped (2^-126 is zero for P's purposes).  Half of each row's
+// exponentials run here instead of on the special-function unit, whose
+// throughput otherwise bounds the softmax.
+__device__ __forceinline__ float poly_exp2(float x) {
+    x = fmaxf(x, -126.0f);
+    const float t = x + 12582912.0f;
+    const float f = x - (t - 12582912.0f);
+    float p = fmaf(f, 0.0096181291076285f, 0.0555041086648216f);
+    p = fmaf(p, f, 0.2402265069591007f);
+    p = fmaf(p, f, 0.6931471805599453f);
+    p = fmaf(p, f, 1.0f);
+    const int n = __float_as_int(t) - 0x4B400000;
+    return __int_as_float(__float_as_int(p) + (n << 23));
+}
+
+// Byte offset of 16-byte chunk c16 (along M/N) of row j (along K) in the
+// 128-byte-swizzled MN-major layout whose 64-element groups are `chunk` apart.
+__device__ __forceinline__ uint32_t swz(int j, int c16, int chunk) {
+    return (uint32_t)((c16 >> 3) * chunk + j * 128 + (((c16 & 7) ^ (j & 7)) << 4));
+}
+
 // Host: raise a kernel's dynamic shared-memory limit to at least `bytes`,
 // once per (device, kernel, size) -- the attribute call costs host time, so
 // later launches skip it.  The limit also matters below 48 KB when the
