@@ -91,7 +91,7 @@ struct TreeArgs {
 };
 
 __device__ __forceinline__ int blocks_of(const TreeArgs& a, int b) {
-    const int len = __ldg(a.lens + b);
+    const int len = a.lens[b];
     return len < 0 || len > a.ldL - a.T ? 0 : (len + a.T + BK - 1) / BK;
 }
 
@@ -129,13 +129,60 @@ __device__ __forceinline__ uint32_t sees32(uint64_t way, int key0, int len) {
     return ((uint32_t)(way << -at)) | (way ? (1u << -at) - 1u : 0u);
 }
 
+// -inf for the 64 logits from key0 on that the row does not see
+__device__ __forceinline__ void hide64(uint32_t (&x)[2][32], uint64_t way, int key0, int len) {
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+        const uint32_t see = sees32(way, key0 + q * 32, len);
+#pragma unroll
+        for (int c = 0; c < 32; ++c)
+            if (!((see >> c) & 1u)) x[q][c] = 0xFF800000u;
+    }
+}
+
+// two fp32 as packed bf16, `lo` in the low half
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// p = 2^(x scale - m) for 64 logits of a row, their sums, and P (bf16) to the 32
+// columns at pcol.  One exponential in four runs on the FMA pipe, which balances
+// it with the special-function unit.  With hidden keys all of them use the unit:
+// its 2^-inf is exactly 0, where the polynomial ends at 2^-126.
+template <bool kHidden>
+__device__ __forceinline__ void exp64(const uint32_t (&x)[2][32], float scale_log2, float neg_m, float (&sm)[4],
+                                      uint32_t pcol) {
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+        uint32_t pk[16];
+#pragma unroll
+        for (int c = 0; c < 32; c += 4) {
+            float p[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float y = fmaf(__uint_as_float(x[q][c + e]), scale_log2, neg_m);
+                p[e] = !kHidden && e == 3 ? poly_exp2(y) : fast_exp2(y);
+                sm[e] += p[e];
+            }
+            pk[c / 2] = pack2(p[0], p[1]);
+            pk[c / 2 + 1] = pack2(p[2], p[3]);
+        }
+        tmem_st_32x32b_x16(pcol + q * 16, pk);
+    }
+}
+
+// kAll: every head dimension kept (Q a tile copy, K-major; key blocks tile copies).
+template <bool kAll>
 __global__ void __launch_bounds__(kThreadsTree, 1)
     attn_tree_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
                      const __grid_constant__ CUtensorMap vmap, const TreeArgs a) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~static_cast<uintptr_t>(1023));
-    const int QK_BYTES = a.kp * 256;  // a query tile or a key block
+    const int kp = kAll ? D : a.kp;
+    const int QK_BYTES = kp * 256;  // a query tile or a key block
     uint8_t* sV = smem;
     uint8_t* sK = sV + a.nv * V_BYTES;
     uint8_t* sQ = sK + a.nk * QK_BYTES;
@@ -146,7 +193,7 @@ __global__ void __launch_bounds__(kThreadsTree, 1)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
     if (tid == 0) {
-        mbar_init(smem_addr(&bars->q_full), a.identity ? 1 : kSoftmaxThreads);
+        mbar_init(smem_addr(&bars->q_full), kAll ? 1 : kSoftmaxThreads);
         mbar_init(smem_addr(&bars->o_full), 1);
         mbar_init(smem_addr(&bars->drain), 1);
         for (int s = 0; s < kMaxStages; ++s) {
@@ -182,7 +229,7 @@ __global__ void __launch_bounds__(kThreadsTree, 1)
         long long total = 0;
         for (int b = lane; b < a.B; b += 32) {
             total += blocks_of(a, b);
-            if (c == 0 && __ldg(a.lens + b) > a.ldL - a.T) record_status(status, RMM_ERR_INVALID_ARG);
+            if (c == 0 && a.lens[b] > a.ldL - a.T) record_status(status, RMM_ERR_INVALID_ARG);
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
@@ -230,7 +277,7 @@ __global__ void __launch_bounds__(kThreadsTree, 1)
         for (bool more = w.next(a, bars, true); ok && more; more = w.next(a, bars, false)) {
             const int plane = w.b * a.Hkv + w.u / a.nrp;
             int r0 = 0, r1 = 0, r2 = 0, r3 = 0;
-            if (!a.identity && lane * 4 < a.kp) {  // this lane's four kept rows of K^T
+            if (!kAll && lane * 4 < kp) {  // this lane's four kept rows of K^T
                 const int32_t* S = a.idx + (size_t)plane * a.k + lane * 4;
                 r0 = lane * 4 + 0 < a.k ? plane * D + S[0] : oob;
                 r1 = lane * 4 + 1 < a.k ? plane * D + S[1] : oob;
@@ -248,14 +295,14 @@ __global__ void __launch_bounds__(kThreadsTree, 1)
                 const uint32_t kb = smem_addr(sK + ks * QK_BYTES), kf = smem_addr(&bars->k_full[ks]);
                 if (lane == 0) mbar_arrive_expect_tx(kf, QK_BYTES);
                 __syncwarp();
-                if (a.identity) {
+                if (kAll) {
                     if (lane == 0) {
                         tma_load_3d(kb, &kmap, kf, key0, 0, plane);
                         tma_load_3d(kb + D * 128, &kmap, kf, key0 + 64, 0, plane);
                     }
-                } else if (lane * 4 < a.kp) {
+                } else if (lane * 4 < kp) {
                     tma_gather4(kb + lane * 512, &kmap, kf, key0, r0, r1, r2, r3);
-                    tma_gather4(kb + a.kp * 128 + lane * 512, &kmap, kf, key0 + 64, r0, r1, r2, r3);
+                    tma_gather4(kb + kp * 128 + lane * 512, &kmap, kf, key0 + 64, r0, r1, r2, r3);
                 }
                 const bool got = mbar_wait(smem_addr(&bars->v_empty[vs]), ((uint32_t)(c / a.nv) & 1u) ^ 1u, status,
                                            abort_flag);
@@ -287,107 +334,85 @@ __global__ void __launch_bounds__(kThreadsTree, 1)
         }
         __syncwarp();
     } else if (warp == kMmaWarp) {
-        // ------------------------------------------------------------ MMA issuer
-        const uint32_t idesc_s = idesc_bf16_f32(BM, BK, a.identity ? 0 : 1, 1);
-        const uint32_t idesc_pv = idesc_bf16_f32(BM, D, 0, 1);
-        int kc0 = 0;           // blocks of the pieces before
-        int pc[2] = {0, 0};    // P.V products issued per group
-        int piece = 0;
-        bool ok = true;
-        for (bool more = w.next(a, bars, true); ok && more; more = w.next(a, bars, false), ++piece) {
-            const int rp = w.u % a.nrp;
-            const bool two = 2 * rp + 1 < a.nrt;
-            const int steps = two ? 2 * w.n : w.n;
-            const int len = __ldg(a.lens + w.b);
-            ok = __all_sync(0xffffffffu, mbar_wait(smem_addr(&bars->q_full), (uint32_t)piece & 1u, status, abort_flag));
-            auto issue_s = [&](int s) -> bool {
-                const int g = s & 1, c = kc0 + (two ? s >> 1 : s), ks = c % a.nk;
-                bool got = mbar_wait(smem_addr(&bars->k_full[ks]), (uint32_t)(c / a.nk) & 1u, status, abort_flag);
-                // P.V of the group's step before has read P, which lies over S
-                if (pc[g] > 0)
-                    got = got && mbar_wait(smem_addr(&bars->pv_done[g]), (uint32_t)(pc[g] - 1) & 1u, status, abort_flag);
-                if (!__all_sync(0xffffffffu, got)) return false;
-                tc_fence_after();
-                if (lane == 0) {
-                    const uint32_t qb = smem_addr(sQ + (two ? g : 0) * QK_BYTES), kb = smem_addr(sK + ks * QK_BYTES);
-                    for (int kk = 0; kk < a.kp / 16; ++kk) {
-                        const uint64_t qd = a.identity
-                                                ? smem_desc_sw128(qb + (kk >> 2) * (BM * 128) + (kk & 3) * 32, 16, 1024)
-                                                : smem_desc_sw128(qb + kk * 2048, a.kp * 128, 1024);
-                        umma_f16(tmem + g * BK, qd, smem_desc_sw128(kb + kk * 2048, a.kp * 128, 1024), idesc_s,
-                                 kk > 0 ? 1u : 0u);
-                    }
-                    umma_commit(smem_addr(&bars->s_full[g]));
-                    if (!two || g == 1) umma_commit(smem_addr(&bars->k_empty[ks]));
-                }
-                __syncwarp();
-                return true;
-            };
-            if (ok) {
+        // ------------------------------------------------------------ MMA issuer: one thread
+        if (lane == 0) {
+            const uint32_t idesc_s = idesc_bf16_f32(BM, BK, kAll ? 0 : 1, 1);
+            const uint32_t idesc_pv = idesc_bf16_f32(BM, D, 0, 1);
+            const uint64_t qd0 = smem_desc_sw128(smem_addr(sQ), kAll ? 16 : kp * 128, 1024);
+            const uint64_t kd0 = smem_desc_sw128(smem_addr(sK), kp * 128, 1024);
+            const uint64_t vd0 = smem_desc_sw128(smem_addr(sV), V_CHUNK, 1024);
+            const int k_steps = kp / 16;
+            int c0 = 0;               // blocks of the pieces before
+            int pv0 = 0, pv1 = 0;     // P.V products issued for each group
+            int piece = 0;
+            bool ok = true;
+            for (bool more = w.next(a, bars, true); ok && more; more = w.next(a, bars, false), ++piece) {
+                const bool two = 2 * (w.u % a.nrp) + 1 < a.nrt;
+                const int steps = two ? 2 * w.n : w.n;
+                ok = mbar_wait(smem_addr(&bars->q_full), (uint32_t)piece & 1u, status, abort_flag);
                 fence_proxy_async_smem();  // a gathered query operand, written by the softmax warps
-                tc_fence_after();
-                ok = issue_s(0);
-            }
-            if (ok && steps > 1) ok = issue_s(1);
-            for (int s = 0; ok && s < steps; ++s) {
-                const int g = s & 1, j = two ? s >> 1 : s, c = kc0 + j, vs = c % a.nv;
-                const bool got = mbar_wait(smem_addr(&bars->v_full[vs]), (uint32_t)(c / a.nv) & 1u, status, abort_flag) &&
-                                 mbar_wait(smem_addr(&bars->p_full[g]), (uint32_t)pc[g] & 1u, status, abort_flag);
-                if (!__all_sync(0xffffffffu, got)) {
-                    ok = false;
-                    break;
-                }
-                const uint32_t vb = smem_addr(sV + vs * V_BYTES);
-                const int at = (w.blk + j) * BK - len;  // the block's first key as a slot of the tree
-                if (at + BK > 0 && (!two || g == 0)) {
-                    // slots that no node holds may contain anything: their values become zeros
-                    uint64_t there = ~0ull >> (kTreeMax - a.T);
-                    if (a.parents) {
-                        const uint32_t lo = __ballot_sync(0xffffffffu, lane < a.T && tree_way(par, lane) != 0);
-                        const uint32_t hi = __ballot_sync(0xffffffffu, lane + 32 < a.T && tree_way(par, lane + 32) != 0);
-                        there = (uint64_t)lo | ((uint64_t)hi << 32);
-                    }
-                    for (int i = lane; i < BK * 8; i += 32) {
-                        const int slot = at + (i >> 3);
-                        if (slot >= 0 && (slot >= a.T || !((there >> slot) & 1))) {
-                            st_shared_v4(vb + i * 16, make_uint4(0, 0, 0, 0));
-                            st_shared_v4(vb + V_CHUNK + i * 16, make_uint4(0, 0, 0, 0));
-                        }
-                    }
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                }
-                tc_fence_after();
-                if (lane == 0) {
-                    const bool fresh = two ? j == 0 : s < 2;  // the group's first block of the piece
+                // step s is group s & 1; S runs two steps ahead of P.V
+                for (int s = -2; ok && s < steps; ++s) {
+                    const int g = s & 1;
+                    if (s >= 0) {
+                        const int c = c0 + (two ? s >> 1 : s), vs = c % a.nv;
+                        int& pv = g ? pv1 : pv0;
+                        ok = mbar_wait(smem_addr(&bars->v_full[vs]), (uint32_t)(c / a.nv) & 1u, status, abort_flag) &&
+                             mbar_wait(smem_addr(&bars->p_full[g]), (uint32_t)pv & 1u, status, abort_flag);
+                        if (!ok) break;
+                        tc_fence_after();
+                        const bool fresh = s < 2;  // the group's first block of the piece
+                        uint64_t vd = vd0 + (uint64_t)(vs * (V_BYTES / 16));  // descriptors count 16 bytes
+                        uint32_t pcol = tmem + g * BK;
 #pragma unroll
-                    for (int kk = 0; kk < BK / 16; ++kk)
-                        umma_f16_tmem_a(tmem + TM_O + g * D, tmem + g * BK + kk * 8,
-                                        smem_desc_sw128(vb + kk * 2048, V_CHUNK, 1024), idesc_pv,
-                                        fresh && kk == 0 ? 0u : 1u);
-                    umma_commit(smem_addr(&bars->pv_done[g]));
-                    if (!two || g == 1) umma_commit(smem_addr(&bars->v_empty[vs]));
+                        for (int kk = 0; kk < BK / 16; ++kk)
+                            umma_f16_tmem_a(tmem + TM_O + g * D, pcol + kk * 8, vd + kk * 128, idesc_pv,
+                                            kk > 0 || !fresh ? 1u : 0u);
+                        umma_commit(smem_addr(&bars->pv_done[g]));
+                        if (!two || g == 1) umma_commit(smem_addr(&bars->v_empty[vs]));
+                        ++pv;
+                    }
+                    if (s + 2 < steps) {
+                        const int c = c0 + (two ? (s + 2) >> 1 : s + 2), ks = c % a.nk;
+                        const int pv = g ? pv1 : pv0;
+                        ok = mbar_wait(smem_addr(&bars->k_full[ks]), (uint32_t)(c / a.nk) & 1u, status, abort_flag);
+                        // P.V of the group's step before has read P, which lies over S
+                        if (ok && pv > 0)
+                            ok = mbar_wait(smem_addr(&bars->pv_done[g]), (uint32_t)(pv - 1) & 1u, status, abort_flag);
+                        if (!ok) break;
+                        tc_fence_after();
+                        uint64_t qd = qd0 + (uint64_t)((two ? g : 0) * (QK_BYTES / 16));
+                        uint64_t kd = kd0 + (uint64_t)(ks * (QK_BYTES / 16));
+                        if (kAll) {
+#pragma unroll
+                            for (int kk = 0; kk < D / 16; ++kk)
+                                umma_f16(tmem + g * BK, qd + (kk >> 2) * (BM * 8) + (kk & 3) * 2, kd + kk * 128, idesc_s,
+                                         kk > 0 ? 1u : 0u);
+                        } else {
+#pragma unroll 1
+                            for (int kk = 0; kk < k_steps; ++kk, qd += 128, kd += 128)
+                                umma_f16(tmem + g * BK, qd, kd, idesc_s, kk > 0 ? 1u : 0u);
+                        }
+                        umma_commit(smem_addr(&bars->s_full[g]));
+                        if (!two || g == 1) umma_commit(smem_addr(&bars->k_empty[ks]));
+                    }
                 }
-                __syncwarp();
-                ++pc[g];
-                if (s + 2 < steps) ok = issue_s(s + 2);
+                if (ok) umma_commit(smem_addr(&bars->o_full));
+                c0 += w.n;
             }
-            if (ok && lane == 0) umma_commit(smem_addr(&bars->o_full));
-            __syncwarp();
-            kc0 += w.n;
+            umma_commit(smem_addr(&bars->drain));
+            // issued MMAs finish on their own; TMEM is not freed under them
+            volatile int no_abort = 0;
+            mbar_wait(smem_addr(&bars->drain), 0, status, &no_abort);
         }
-        if (lane == 0) umma_commit(smem_addr(&bars->drain));
         __syncwarp();
-        // issued MMAs finish on their own; TMEM is not freed under them
-        volatile int no_abort = 0;
-        mbar_wait(smem_addr(&bars->drain), 0, status, &no_abort);
     } else {
         // ------------------------------------------------------------ softmax, query operand, output
         const int grp = warp >> 2, i = tid & 127;  // group, row of the tile = TMEM lane
         const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t s_col = tmem + lane_base + grp * BK, meet = smem_addr(&bars->meet);
         float* xch = reinterpret_cast<float*>(sQ);  // maxima and sums of the two groups (sQ is free by then)
-        int steps_done = 0, piece = 0, meets = 0, queries = 0;
+        int steps_done = 0, piece = 0, meets = 0, queries = 0, c0 = 0;
         // all softmax warps meet (bounded)
         auto together = [&]() -> bool {
             __syncwarp();
@@ -399,7 +424,7 @@ __global__ void __launch_bounds__(kThreadsTree, 1)
             const int g = w.u / a.nrp, rp = w.u % a.nrp;
             const bool two = 2 * rp + 1 < a.nrt;
             const int plane = w.b * a.Hkv + g;
-            const int len = __ldg(a.lens + w.b);
+            const int len = a.lens[w.b];
             const int tile = 2 * rp + (two ? grp : 0);
             const int row = tile * BM + i;  // of the unit's G * T rows: query head row / T, node row % T
             const size_t row0 = (size_t)plane * a.R;
@@ -407,8 +432,8 @@ __global__ void __launch_bounds__(kThreadsTree, 1)
             // maxima and sums that lay where a copy now writes)
             fence_proxy_async_smem();
             if (!together()) break;
-            if (a.parents && tid < a.T) par[tid] = __ldg(a.parents + (size_t)w.b * a.T + tid);
-            if (a.identity) {
+            if (a.parents && tid < a.T) par[tid] = a.parents[(size_t)w.b * a.T + tid];
+            if (kAll) {
                 if (tid == 0) {
                     const uint32_t qf = smem_addr(&bars->q_full), qb = smem_addr(sQ);
                     mbar_arrive_expect_tx(qf, (two ? 2 : 1) * BM * 256);
@@ -423,15 +448,15 @@ __global__ void __launch_bounds__(kThreadsTree, 1)
                 // the kept dims of 8 rows at a time; both groups share the work of one tile
                 const int32_t* S = a.idx + (size_t)plane * a.k;
                 const int tiles = two ? 2 : 1;
-                for (int it = tid; it < a.kp * 16 * tiles; it += kSoftmaxThreads) {
-                    const int jr = it % a.kp, c16 = (it / a.kp) & 15, t = it / (a.kp * 16);
-                    const int dim = jr < a.k ? __ldg(S + jr) : -1;
+                for (int it = tid; it < kp * 16 * tiles; it += kSoftmaxThreads) {
+                    const int jr = it % kp, c16 = (it / kp) & 15, t = it / (kp * 16);
+                    const int dim = jr < a.k ? S[jr] : -1;
                     const int r = (2 * rp + t) * BM + c16 * 8;
                     uint16_t v[8];
 #pragma unroll
                     for (int e = 0; e < 8; ++e)
                         v[e] = dim >= 0 && r + e < a.R ? a.Q[(row0 + r + e) * D + dim] : (uint16_t)0;
-                    st_shared_v4(smem_addr(sQ + t * QK_BYTES) + swz(jr, c16, a.kp * 128),
+                    st_shared_v4(smem_addr(sQ + t * QK_BYTES) + swz(jr, c16, kp * 128),
                                  make_uint4(v[0] | ((uint32_t)v[1] << 16), v[2] | ((uint32_t)v[3] << 16),
                                             v[4] | ((uint32_t)v[5] << 16), v[6] | ((uint32_t)v[7] << 16)));
                 }
@@ -454,25 +479,20 @@ __global__ void __launch_bounds__(kThreadsTree, 1)
                 tc_fence_after();
                 if (busy) {
                     const int key0 = (w.blk + (two ? s : 2 * s + grp)) * BK;
-                    uint32_t x[4][32];
+                    const bool mask = key0 + BK > len;  // the block reaches the tree's slots
+                    // S is read twice, 64 columns at a time: kept whole it spills (128 values a
+                    // thread), and with nearly all of L1 given to shared memory a spill goes to L2
+                    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) tmem_ld_32x32b_x32(s_col + q * 32, x[q]);
-                    tmem_ld_wait();
-                    if (key0 + BK > len) {  // the block reaches the tree's slots
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t x[2][32];
+                        tmem_ld_32x32b_x32(s_col + h * 64, x[0]);
+                        tmem_ld_32x32b_x32(s_col + h * 64 + 32, x[1]);
+                        tmem_ld_wait();
+                        if (mask) hide64(x, way, key0 + h * 64, len);
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            const uint32_t see = sees32(way, key0 + q * 32, len);
-#pragma unroll
-                            for (int c = 0; c < 32; ++c)
-                                if (!((see >> c) & 1u)) x[q][c] = 0xFF800000u;  // -inf
-                        }
-                    }
-                    float mx[4];
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        mx[q] = __uint_as_float(x[q][0]);
-#pragma unroll
-                        for (int c = 1; c < 32; ++c) mx[q] = fmaxf(mx[q], __uint_as_float(x[q][c]));
+                        for (int c = 0; c < 64; ++c)
+                            mx[c & 3] = fmaxf(mx[c & 3], __uint_as_float(x[c >> 5][c & 31]));
                     }
                     const float m_blk = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2;
                     const bool resc = m_blk > m_use + kRescaleLog2;
@@ -495,29 +515,47 @@ __global__ void __launch_bounds__(kThreadsTree, 1)
                     m_use = m_new;
                     float sm[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        uint32_t pk[16];
-#pragma unroll
-                        for (int c = 0; c < 32; c += 2) {
-                            const float y0 = fmaf(__uint_as_float(x[q][c]), a.scale_log2, neg_m);
-                            const float y1 = fmaf(__uint_as_float(x[q][c + 1]), a.scale_log2, neg_m);
-                            const float p0 = fast_exp2(y0);
-                            // the polynomial ends at 2^-126, which P rounds to no weight next to a
-                            // row's largest; a masked key's weight is exactly 0
-                            const float p1 = y1 < -126.0f ? 0.0f : poly_exp2(y1);
-                            sm[(c >> 1) & 3] += p0 + p1;
-                            pk[c >> 1] = pack_bf16x2(p0, p1);
-                        }
-                        tmem_st_32x32b_x16(s_col + q * 16, pk);  // P over columns of S that are already read
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t x[2][32];
+                        tmem_ld_32x32b_x32(s_col + h * 64, x[0]);
+                        tmem_ld_32x32b_x32(s_col + h * 64 + 32, x[1]);
+                        tmem_ld_wait();
+                        if (mask) hide64(x, way, key0 + h * 64, len);
+                        // P over columns of S already read
+                        if (mask)
+                            exp64<true>(x, a.scale_log2, neg_m, sm, s_col + h * 32);
+                        else
+                            exp64<false>(x, a.scale_log2, neg_m, sm, s_col + h * 32);
                     }
                     tmem_st_wait();
                     l = l * alpha + ((sm[0] + sm[1]) + (sm[2] + sm[3]));
+                }
+                const int j = two ? s : 2 * s + grp, at = (w.blk + j) * BK - len;
+                if (at + BK > 0 && (!two || grp == 0)) {
+                    // slots that no node holds may contain anything: their values become zeros,
+                    // a thread per key
+                    const int vs = (c0 + j) % a.nv, slot = at + i;
+                    if (!__all_sync(0xffffffffu, mbar_wait(smem_addr(&bars->v_full[vs]), (uint32_t)((c0 + j) / a.nv) & 1u,
+                                                           status, abort_flag))) {
+                        ok = false;
+                        break;
+                    }
+                    if (slot >= a.T || (slot >= 0 && a.parents && tree_way(par, slot) == 0)) {
+                        const uint32_t v = smem_addr(sV + vs * V_BYTES) + i * 128;
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            st_shared_v4(v + ((e + lane) & 7) * 16, make_uint4(0, 0, 0, 0));
+                            st_shared_v4(v + V_CHUNK + ((e + lane) & 7) * 16, make_uint4(0, 0, 0, 0));
+                        }
+                    }
+                    fence_proxy_async_smem();
                 }
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_addr(&bars->p_full[grp]));
             }
             if (!ok) break;
+            c0 += w.n;
             if (!__all_sync(0xffffffffu,
                             mbar_wait(smem_addr(&bars->o_full), (uint32_t)piece & 1u, status, abort_flag))) {
                 ok = false;
@@ -687,7 +725,7 @@ __global__ void __launch_bounds__(256) tree_dims_kernel(const TreeArgs a) {
     uint64_t there = ~0ull;
     if (a.parents) {
         if (tid == 0) there_s = 0;
-        if (tid < a.T) par[tid] = __ldg(a.parents + (size_t)b * a.T + tid);
+        if (tid < a.T) par[tid] = a.parents[(size_t)b * a.T + tid];
         __syncthreads();
         if (tid < a.T && tree_way(par, tid))
             atomicOr(reinterpret_cast<unsigned long long*>(&there_s), 1ull << tid);
@@ -790,13 +828,14 @@ cudaError_t launch_attn_tree(const CUtensorMap& qmap, const CUtensorMap& kmap, c
         if (a.nk < kMaxStages && a.nk < a.nv && fixed + a.nv * V_BYTES + (a.nk + 1) * qk <= kSmemMax) ++a.nk, grew = true;
     }
     const size_t smem = fixed + (size_t)a.nv * V_BYTES + (size_t)a.nk * qk;
-    cudaError_t e = ensure_smem_limit(attn_tree_kernel, smem);
+    auto* kern = a.identity ? attn_tree_kernel<true> : attn_tree_kernel<false>;
+    cudaError_t e = ensure_smem_limit(kern, smem);
     if (e != cudaSuccess) return e;
     if (!a.identity) {
         e = launch_pdl(tree_dims_kernel, dim3(B * Hkv), dim3(256), 0, stream, a);
         if (e != cudaSuccess) return e;
     }
-    e = launch_pdl(attn_tree_kernel, dim3(p.ctas), dim3(kThreadsTree), smem, stream, qmap, kmap, vmap, a);
+    e = launch_pdl(kern, dim3(p.ctas), dim3(kThreadsTree), smem, stream, qmap, kmap, vmap, a);
     if (e != cudaSuccess) return e;
     const int most_rows = p.R < 2 * BM ? p.R : 2 * BM;
     return launch_pdl(attn_tree_join_kernel, dim3(B * Hkv * p.nrp, (most_rows * 32 + 255) / 256), dim3(256), 0, stream, a,

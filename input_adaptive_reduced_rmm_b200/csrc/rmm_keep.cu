@@ -20,8 +20,8 @@ constexpr int D = 128;
 constexpr int kKeepThreads = 256;
 
 __global__ void __launch_bounds__(kKeepThreads)
-    cache_keep_kernel(const __grid_constant__ CacheList caches, int Hkv, int ldL, const int32_t* __restrict__ lens,
-                      const int32_t* __restrict__ path, const int32_t* __restrict__ count, int T, int32_t* lens_out) {
+    cache_keep_kernel(const __grid_constant__ CacheList caches, int Hkv, int ldL, const int32_t* lens,
+                      const int32_t* path, const int32_t* count, int T, int32_t* lens_out) {
     __shared__ int from[kTreeMax];
     const int g = blockIdx.x, b = blockIdx.y, layer = blockIdx.z;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -74,8 +74,8 @@ __global__ void __launch_bounds__(kKeepThreads)
 
 // The lengths alone, after the move, when they are updated in place: the CTAs of
 // the move all read the old ones.
-__global__ void grow_lens_kernel(int B, int T, int ldL, int32_t* lens, const int32_t* __restrict__ path,
-                                 const int32_t* __restrict__ count) {
+__global__ void grow_lens_kernel(int B, int T, int ldL, int32_t* lens, const int32_t* path,
+                                 const int32_t* count) {
     pdl_wait();
     pdl_launch_dependents();
     const int b = blockIdx.x * blockDim.x + threadIdx.x;

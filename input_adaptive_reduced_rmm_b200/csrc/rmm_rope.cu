@@ -74,10 +74,10 @@ __global__ void __launch_bounds__(kRopeThreads) qkv_rope_kernel(const RopeArgs a
     const int nh = min(kRopeHeads, H - h0);
     pdl_wait();
     pdl_launch_dependents();
-    const int start = a.lens ? __ldg(a.lens + b) : a.L0;
+    const int start = a.lens ? a.lens[b] : a.L0;
     if (start < 0 || start > a.ldL - a.T) return;  // an empty slot of the batch, or no room: nothing is written
     if (a.parents) {
-        if (tid < a.T) par[tid] = __ldg(a.parents + (size_t)b * a.T + tid);
+        if (tid < a.T) par[tid] = a.parents[(size_t)b * a.T + tid];
         __syncthreads();
     }
     if (tid < nt) {

@@ -39,7 +39,7 @@ __device__ __forceinline__ void merge(float& m, float& s, float m2, float s2, fl
 // boundaries; wide_y: rows of Y do.
 template <int NV>
 __global__ void __launch_bounds__(kThreads)
-    softmax_kernel(const uint16_t* __restrict__ X, int V, int64_t ldx, float c, int one_hot, float* __restrict__ Y,
+    softmax_kernel(const uint16_t* X, int V, int64_t ldx, float c, int one_hot, float* Y,
                    int64_t ldy, int nc, int wide, int wide_y) {
     __shared__ float red_m[kThreads / 32], red_s[kThreads / 32];
     __shared__ int red_i[kThreads / 32];

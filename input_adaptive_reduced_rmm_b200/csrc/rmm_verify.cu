@@ -67,10 +67,10 @@ __device__ __forceinline__ double remaining(double r, double q, int i, bool draw
 }
 
 __global__ void __launch_bounds__(kThreads)
-    tree_verify_kernel(const float* __restrict__ P, int64_t ldp, const float* __restrict__ Qd, int64_t ldq, int V,
-                       int T, const int32_t* __restrict__ tokens, const int32_t* __restrict__ parents,
-                       const float* __restrict__ u, int32_t* __restrict__ path, int32_t* __restrict__ emitted,
-                       int32_t* __restrict__ count, int per_warp, int wide) {
+    tree_verify_kernel(const float* P, int64_t ldp, const float* Qd, int64_t ldq, int V,
+                       int T, const int32_t* tokens, const int32_t* parents,
+                       const float* u, int32_t* path, int32_t* emitted,
+                       int32_t* count, int per_warp, int wide) {
     __shared__ int par[kTreeMax], tok[kTreeMax], way[kTreeMax];
     __shared__ double pv[kTreeMax], qv[kTreeMax], uv[kTreeMax];
     __shared__ Walk w;
@@ -113,8 +113,8 @@ __global__ void __launch_bounds__(kThreads)
         if (wide) {
             for (int i = lo + lane * 4; i < hi; i += 128) {
                 if (i + 4 <= hi) {
-                    const float4 a = __ldg(reinterpret_cast<const float4*>(p + i));
-                    const float4 c = drawn ? __ldg(reinterpret_cast<const float4*>(q + i)) : a;
+                    const float4 a = *reinterpret_cast<const float4*>(p + i);
+                    const float4 c = drawn ? *reinterpret_cast<const float4*>(q + i) : a;
                     acc += remaining(prob(a.x), prob(c.x), i, drawn, n_rej, w);
                     acc += remaining(prob(a.y), prob(c.y), i + 1, drawn, n_rej, w);
                     acc += remaining(prob(a.z), prob(c.z), i + 2, drawn, n_rej, w);
