@@ -30,9 +30,9 @@
 //   warps 0-7  softmax: S from TMEM, mask, running maximum, P (bf16) over S's own
 //              columns, O rescaled only when the maximum grew by more than 2^8;
 //              the query operand at the start of a unit, its output at the end
-//   warp 8     MMA: S = Q_S K_S^T for a group's next step as soon as its P.V is
-//              done, P.V (A from TMEM) as soon as its P is written
-//   warp 9     TMA: key and value blocks through two rings, running ahead over
+//   warps 8, 9 MMA, a thread for each group: S = Q_S K_S^T for the group's next step
+//              as soon as its P.V is done, P.V (A from TMEM) as soon as its P is written
+//   warp 10    TMA: key and value blocks through two rings, running ahead over
 //              units.  With every dim kept the key block is two tile copies of
 //              the d-major cache; else the kept rows come by tile::gather4.
 //
@@ -55,10 +55,11 @@ namespace {
 constexpr int D = 128;
 constexpr int BM = 128;  // rows per tile (= TMEM lanes)
 constexpr int BK = 128;  // keys per block
+constexpr int HK = 64;   // keys per half: the step of S, softmax and P.V
 constexpr int kMaxStages = 6;
 constexpr int kSoftmaxThreads = 256;
-constexpr int kMmaWarp = 8, kTmaWarp = 9;
-constexpr int kThreadsTree = 320;
+constexpr int kMmaWarp = 8, kTmaWarp = 10;  // MMA warps 8 and 9: one per group
+constexpr int kThreadsTree = 384;
 constexpr int V_CHUNK = BK * 128;  // 64 dims of a value block
 constexpr int V_BYTES = 2 * V_CHUNK;
 constexpr uint32_t TM_O = 256;  // S of group a at 128 a, O of group a at 256 + 128 a
@@ -69,7 +70,8 @@ struct __align__(8) TreeBars {
     uint64_t q_full, o_full, drain;
     uint64_t k_full[kMaxStages], k_empty[kMaxStages];
     uint64_t v_full[kMaxStages], v_empty[kMaxStages];
-    uint64_t s_full[2], p_full[2], pv_done[2];
+    uint64_t s_full[2][2], p_full[2][2];  // [group][half of the block]
+    uint64_t pv_done[2];
     uint64_t meet;  // all softmax warps
     long long pos;  // the CTA's share: first block, and how many
     int seg_b, seg_u, seg_blk, blocks;
@@ -118,6 +120,16 @@ struct Share {
     }
 };
 
+// A place in a ring of stages: its slot and the parity of its round.
+struct Ring {
+    int slot = 0;
+    uint32_t phase = 0;
+    __device__ __forceinline__ void next(int by, int n) {  // by <= n
+        slot += by;
+        if (slot >= n) slot -= n, phase ^= 1u;
+    }
+};
+
 // floats of one partial: O in pieces of four dims [32][rows][4], then maxima, then sums
 __host__ __device__ constexpr size_t slot_floats(int rows) { return (size_t)rows * (D + 2); }
 
@@ -129,8 +141,8 @@ __device__ __forceinline__ uint32_t sees32(uint64_t way, int key0, int len) {
     return ((uint32_t)(way << -at)) | (way ? (1u << -at) - 1u : 0u);
 }
 
-// -inf for the 64 logits from key0 on that the row does not see
-__device__ __forceinline__ void hide64(uint32_t (&x)[2][32], uint64_t way, int key0, int len) {
+// -inf for the keys from key0 on that the row does not see
+__device__ __forceinline__ void hide(uint32_t (&x)[2][32], uint64_t way, int key0, int len) {
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
         const uint32_t see = sees32(way, key0 + q * 32, len);
@@ -140,6 +152,13 @@ __device__ __forceinline__ void hide64(uint32_t (&x)[2][32], uint64_t way, int k
     }
 }
 
+// the largest of three
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
 // two fp32 as packed bf16, `lo` in the low half
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     uint32_t r;
@@ -147,30 +166,24 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     return r;
 }
 
-// p = 2^(x scale - m) for 64 logits of a row, their sums, and P (bf16) to the 32
-// columns at pcol.  One exponential in four runs on the FMA pipe, which balances
-// it with the special-function unit.  With hidden keys all of them use the unit:
-// its 2^-inf is exactly 0, where the polynomial ends at 2^-126.
-template <bool kHidden>
-__device__ __forceinline__ void exp64(const uint32_t (&x)[2][32], float scale_log2, float neg_m, float (&sm)[4],
-                                      uint32_t pcol) {
+// p = 2^(x scale - m) for 64 logits of a row, their sum, and P (bf16) to the 32
+// columns at pcol.
+__device__ __forceinline__ float exp_half(const uint32_t (&x)[2][32], float scale_log2, float neg_m, uint32_t pcol) {
+    float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
         uint32_t pk[16];
 #pragma unroll
-        for (int c = 0; c < 32; c += 4) {
-            float p[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float y = fmaf(__uint_as_float(x[q][c + e]), scale_log2, neg_m);
-                p[e] = !kHidden && e == 3 ? poly_exp2(y) : fast_exp2(y);
-                sm[e] += p[e];
-            }
-            pk[c / 2] = pack2(p[0], p[1]);
-            pk[c / 2 + 1] = pack2(p[2], p[3]);
+        for (int c = 0; c < 32; c += 2) {
+            const float p0 = fast_exp2(fmaf(__uint_as_float(x[q][c]), scale_log2, neg_m));
+            const float p1 = fast_exp2(fmaf(__uint_as_float(x[q][c + 1]), scale_log2, neg_m));
+            sum[c & 2] += p0;
+            sum[(c & 2) + 1] += p1;
+            pk[c >> 1] = pack2(p0, p1);
         }
         tmem_st_32x32b_x16(pcol + q * 16, pk);
     }
+    return (sum[0] + sum[1]) + (sum[2] + sum[3]);
 }
 
 // kAll: every head dimension kept (Q a tile copy, K-major; key blocks tile copies).
@@ -192,19 +205,22 @@ __global__ void __launch_bounds__(kThreadsTree, 1)
     int* status = a.status;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
+    const int users = a.nrt > 1 ? 2 : 1;  // groups that release a block
     if (tid == 0) {
         mbar_init(smem_addr(&bars->q_full), kAll ? 1 : kSoftmaxThreads);
-        mbar_init(smem_addr(&bars->o_full), 1);
-        mbar_init(smem_addr(&bars->drain), 1);
+        mbar_init(smem_addr(&bars->o_full), 2);
+        mbar_init(smem_addr(&bars->drain), 2);
         for (int s = 0; s < kMaxStages; ++s) {
             mbar_init(smem_addr(&bars->k_full[s]), 1);
-            mbar_init(smem_addr(&bars->k_empty[s]), 1);
+            mbar_init(smem_addr(&bars->k_empty[s]), users);
             mbar_init(smem_addr(&bars->v_full[s]), 1);
-            mbar_init(smem_addr(&bars->v_empty[s]), 1);
+            mbar_init(smem_addr(&bars->v_empty[s]), users);
         }
         for (int s = 0; s < 2; ++s) {
-            mbar_init(smem_addr(&bars->s_full[s]), 1);
-            mbar_init(smem_addr(&bars->p_full[s]), 4);
+            for (int h = 0; h < 2; ++h) {
+                mbar_init(smem_addr(&bars->s_full[s][h]), 1);
+                mbar_init(smem_addr(&bars->p_full[s][h]), 4);
+            }
             mbar_init(smem_addr(&bars->pv_done[s]), 1);
         }
         mbar_init(smem_addr(&bars->meet), 8);
@@ -272,6 +288,7 @@ __global__ void __launch_bounds__(kThreadsTree, 1)
     if (warp == kTmaWarp) {
         // ------------------------------------------------------------ key and value blocks
         int c = 0;  // blocks issued
+        Ring k, v;
         bool ok = true;
         const int oob = a.B * a.Hkv * D;  // a row outside the key map: reads as zeros
         for (bool more = w.next(a, bars, true); ok && more; more = w.next(a, bars, false)) {
@@ -286,13 +303,11 @@ __global__ void __launch_bounds__(kThreadsTree, 1)
             }
             for (int j = 0; j < w.n; ++j, ++c) {
                 const int key0 = (w.blk + j) * BK;
-                const int ks = c % a.nk, vs = c % a.nv;
-                if (!__all_sync(0xffffffffu, mbar_wait(smem_addr(&bars->k_empty[ks]), ((uint32_t)(c / a.nk) & 1u) ^ 1u,
-                                                       status, abort_flag))) {
+                if (!__all_sync(0xffffffffu, mbar_wait(smem_addr(&bars->k_empty[k.slot]), k.phase ^ 1u, status, abort_flag))) {
                     ok = false;
                     break;
                 }
-                const uint32_t kb = smem_addr(sK + ks * QK_BYTES), kf = smem_addr(&bars->k_full[ks]);
+                const uint32_t kb = smem_addr(sK + k.slot * QK_BYTES), kf = smem_addr(&bars->k_full[k.slot]);
                 if (lane == 0) mbar_arrive_expect_tx(kf, QK_BYTES);
                 __syncwarp();
                 if (kAll) {
@@ -304,24 +319,25 @@ __global__ void __launch_bounds__(kThreadsTree, 1)
                     tma_gather4(kb + lane * 512, &kmap, kf, key0, r0, r1, r2, r3);
                     tma_gather4(kb + kp * 128 + lane * 512, &kmap, kf, key0 + 64, r0, r1, r2, r3);
                 }
-                const bool got = mbar_wait(smem_addr(&bars->v_empty[vs]), ((uint32_t)(c / a.nv) & 1u) ^ 1u, status,
-                                           abort_flag);
+                const bool got = mbar_wait(smem_addr(&bars->v_empty[v.slot]), v.phase ^ 1u, status, abort_flag);
                 if (!__all_sync(0xffffffffu, got)) {
                     // this block's keys are on their way, its values are not
                     if (lane == 0) {
                         volatile int no_abort = 0;
-                        mbar_wait(kf, (uint32_t)(c / a.nk) & 1u, status, &no_abort);
+                        mbar_wait(kf, k.phase, status, &no_abort);
                     }
                     ok = false;
                     break;
                 }
                 if (lane == 0) {
-                    const uint32_t vb = smem_addr(sV + vs * V_BYTES), vf = smem_addr(&bars->v_full[vs]);
+                    const uint32_t vb = smem_addr(sV + v.slot * V_BYTES), vf = smem_addr(&bars->v_full[v.slot]);
                     mbar_arrive_expect_tx(vf, V_BYTES);
                     tma_load_3d(vb, &vmap, vf, 0, key0, plane);
                     tma_load_3d(vb + V_CHUNK, &vmap, vf, 64, key0, plane);
                 }
                 __syncwarp();
+                k.next(1, a.nk);
+                v.next(1, a.nv);
             }
         }
         // no copy may still be landing when the CTA leaves (after an abort; else all were consumed)
@@ -333,72 +349,81 @@ __global__ void __launch_bounds__(kThreadsTree, 1)
                 mbar_wait(smem_addr(&bars->v_full[j % a.nv]), (uint32_t)(j / a.nv) & 1u, status, &no_abort);
         }
         __syncwarp();
-    } else if (warp == kMmaWarp) {
-        // ------------------------------------------------------------ MMA issuer: one thread
+    } else if (warp == kMmaWarp || warp == kMmaWarp + 1) {
+        // ------------------------------------------------------------ MMA issuers: a thread per group
         if (lane == 0) {
-            const uint32_t idesc_s = idesc_bf16_f32(BM, BK, kAll ? 0 : 1, 1);
+            const int g = warp - kMmaWarp;
+            const uint32_t idesc_s = idesc_bf16_f32(BM, HK, kAll ? 0 : 1, 1);
             const uint32_t idesc_pv = idesc_bf16_f32(BM, D, 0, 1);
             const uint64_t qd0 = smem_desc_sw128(smem_addr(sQ), kAll ? 16 : kp * 128, 1024);
             const uint64_t kd0 = smem_desc_sw128(smem_addr(sK), kp * 128, 1024);
             const uint64_t vd0 = smem_desc_sw128(smem_addr(sV), V_CHUNK, 1024);
+            const uint32_t s_tm = tmem + g * BK, o_tm = tmem + TM_O + g * D;
+            const uint32_t s_full = smem_addr(&bars->s_full[g][0]), p_full = smem_addr(&bars->p_full[g][0]);
+            const uint32_t pv_done = smem_addr(&bars->pv_done[g]);
             const int k_steps = kp / 16;
-            int c0 = 0;               // blocks of the pieces before
-            int pv0 = 0, pv1 = 0;     // P.V products issued for each group
+            Ring k0, v0;              // the piece's first block
+            uint32_t pv = 0;          // P.V products issued (two per block)
             int piece = 0;
             bool ok = true;
             for (bool more = w.next(a, bars, true); ok && more; more = w.next(a, bars, false), ++piece) {
+                // with two row tiles every block is this group's, with one every second
                 const bool two = 2 * (w.u % a.nrp) + 1 < a.nrt;
-                const int steps = two ? 2 * w.n : w.n;
+                const int by = two ? 1 : 2, steps = two ? w.n : (w.n + 1 - g) / 2;
+                const int releases = two ? 1 : users;  // the group alone releases a block of one tile
+                const uint64_t qd = qd0 + (uint64_t)((two ? g : 0) * (QK_BYTES / 16));  // descriptors count 16 bytes
+                Ring k = k0, v = v0;
+                if (!two && g == 1) k.next(1, a.nk), v.next(1, a.nv);
                 ok = mbar_wait(smem_addr(&bars->q_full), (uint32_t)piece & 1u, status, abort_flag);
                 fence_proxy_async_smem();  // a gathered query operand, written by the softmax warps
-                // step s is group s & 1; S runs two steps ahead of P.V
-                for (int s = -2; ok && s < steps; ++s) {
-                    const int g = s & 1;
-                    if (s >= 0) {
-                        const int c = c0 + (two ? s >> 1 : s), vs = c % a.nv;
-                        int& pv = g ? pv1 : pv0;
-                        ok = mbar_wait(smem_addr(&bars->v_full[vs]), (uint32_t)(c / a.nv) & 1u, status, abort_flag) &&
-                             mbar_wait(smem_addr(&bars->p_full[g]), (uint32_t)pv & 1u, status, abort_flag);
+                // halves of the group's blocks: P.V of one, then S of the same half of the next block,
+                // while the softmax works on the other half
+                for (int n = -2; ok && n < 2 * steps; ++n) {
+                    const int h = n & 1;
+                    if (n >= 0) {
+                        ok = (h || mbar_wait(smem_addr(&bars->v_full[v.slot]), v.phase, status, abort_flag)) &&
+                             mbar_wait(p_full + h * 8, (pv >> 1) & 1u, status, abort_flag);
                         if (!ok) break;
                         tc_fence_after();
-                        const bool fresh = s < 2;  // the group's first block of the piece
-                        uint64_t vd = vd0 + (uint64_t)(vs * (V_BYTES / 16));  // descriptors count 16 bytes
-                        uint32_t pcol = tmem + g * BK;
+                        const uint64_t vd = vd0 + (uint64_t)(v.slot * (V_BYTES / 16) + h * (HK * 8));
 #pragma unroll
-                        for (int kk = 0; kk < BK / 16; ++kk)
-                            umma_f16_tmem_a(tmem + TM_O + g * D, pcol + kk * 8, vd + kk * 128, idesc_pv,
-                                            kk > 0 || !fresh ? 1u : 0u);
-                        umma_commit(smem_addr(&bars->pv_done[g]));
-                        if (!two || g == 1) umma_commit(smem_addr(&bars->v_empty[vs]));
+                        for (int kk = 0; kk < HK / 16; ++kk)
+                            umma_f16_tmem_a(o_tm, s_tm + h * HK + kk * 8, vd + kk * 128, idesc_pv,
+                                            kk > 0 || n > 0 ? 1u : 0u);
+                        umma_commit(pv_done);
+                        if (h) {
+                            for (int r = 0; r < releases; ++r) umma_commit(smem_addr(&bars->v_empty[v.slot]));
+                            v.next(by, a.nv);
+                        }
                         ++pv;
                     }
-                    if (s + 2 < steps) {
-                        const int c = c0 + (two ? (s + 2) >> 1 : s + 2), ks = c % a.nk;
-                        const int pv = g ? pv1 : pv0;
-                        ok = mbar_wait(smem_addr(&bars->k_full[ks]), (uint32_t)(c / a.nk) & 1u, status, abort_flag);
-                        // P.V of the group's step before has read P, which lies over S
-                        if (ok && pv > 0)
-                            ok = mbar_wait(smem_addr(&bars->pv_done[g]), (uint32_t)(pv - 1) & 1u, status, abort_flag);
+                    if (n + 2 < 2 * steps) {
+                        ok = h || mbar_wait(smem_addr(&bars->k_full[k.slot]), k.phase, status, abort_flag);
+                        // the P.V just issued reads P, which lies over this half's S
+                        if (ok && n >= 0) ok = mbar_wait(pv_done, (pv - 1) & 1u, status, abort_flag);
                         if (!ok) break;
                         tc_fence_after();
-                        uint64_t qd = qd0 + (uint64_t)((two ? g : 0) * (QK_BYTES / 16));
-                        uint64_t kd = kd0 + (uint64_t)(ks * (QK_BYTES / 16));
+                        const uint64_t kd = kd0 + (uint64_t)(k.slot * (QK_BYTES / 16) + h * (kp * 8));
                         if (kAll) {
 #pragma unroll
                             for (int kk = 0; kk < D / 16; ++kk)
-                                umma_f16(tmem + g * BK, qd + (kk >> 2) * (BM * 8) + (kk & 3) * 2, kd + kk * 128, idesc_s,
+                                umma_f16(s_tm + h * HK, qd + (kk >> 2) * (BM * 8) + (kk & 3) * 2, kd + kk * 128, idesc_s,
                                          kk > 0 ? 1u : 0u);
                         } else {
+                            uint64_t q1 = qd, k1 = kd;
 #pragma unroll 1
-                            for (int kk = 0; kk < k_steps; ++kk, qd += 128, kd += 128)
-                                umma_f16(tmem + g * BK, qd, kd, idesc_s, kk > 0 ? 1u : 0u);
+                            for (int kk = 0; kk < k_steps; ++kk, q1 += 128, k1 += 128)
+                                umma_f16(s_tm + h * HK, q1, k1, idesc_s, kk > 0 ? 1u : 0u);
                         }
-                        umma_commit(smem_addr(&bars->s_full[g]));
-                        if (!two || g == 1) umma_commit(smem_addr(&bars->k_empty[ks]));
+                        umma_commit(s_full + h * 8);
+                        if (h) {
+                            for (int r = 0; r < releases; ++r) umma_commit(smem_addr(&bars->k_empty[k.slot]));
+                            k.next(by, a.nk);
+                        }
                     }
                 }
                 if (ok) umma_commit(smem_addr(&bars->o_full));
-                c0 += w.n;
+                for (int j = 0; j < w.n; ++j) k0.next(1, a.nk), v0.next(1, a.nv);
             }
             umma_commit(smem_addr(&bars->drain));
             // issued MMAs finish on their own; TMEM is not freed under them
@@ -406,13 +431,17 @@ __global__ void __launch_bounds__(kThreadsTree, 1)
             mbar_wait(smem_addr(&bars->drain), 0, status, &no_abort);
         }
         __syncwarp();
-    } else {
+    } else if (warp < kMmaWarp) {
         // ------------------------------------------------------------ softmax, query operand, output
         const int grp = warp >> 2, i = tid & 127;  // group, row of the tile = TMEM lane
         const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t s_col = tmem + lane_base + grp * BK, meet = smem_addr(&bars->meet);
         float* xch = reinterpret_cast<float*>(sQ);  // maxima and sums of the two groups (sQ is free by then)
-        int steps_done = 0, piece = 0, meets = 0, queries = 0, c0 = 0;
+        int piece = 0, meets = 0, queries = 0;
+        Ring v0;  // the piece's first block in the value ring
+        const uint32_t s_full = smem_addr(&bars->s_full[grp][0]), p_full = smem_addr(&bars->p_full[grp][0]);
+        const uint32_t pv_done = smem_addr(&bars->pv_done[grp]);
+        uint32_t halves = 0;  // of this group, over all pieces
         // all softmax warps meet (bounded)
         auto together = [&]() -> bool {
             __syncwarp();
@@ -470,92 +499,83 @@ __global__ void __launch_bounds__(kThreadsTree, 1)
 
             const int mine = two ? w.n : (w.n + 1 - grp) / 2;  // this group's steps
             float m_use = -INFINITY, l = 0.0f;
-            for (int s = 0; s < mine; ++s, ++steps_done) {
-                if (!__all_sync(0xffffffffu, mbar_wait(smem_addr(&bars->s_full[grp]), (uint32_t)steps_done & 1u, status,
-                                                       abort_flag))) {
+            Ring v = v0;
+            if (!two && grp == 1) v.next(1, a.nv);
+            for (int n = 0; n < 2 * mine; ++n, ++halves) {
+                const int h = n & 1, key0 = (w.blk + (two ? n >> 1 : (n & ~1) + grp)) * BK + h * HK;
+                if (!__all_sync(0xffffffffu, mbar_wait(s_full + h * 8, (halves >> 1) & 1u, status, abort_flag))) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
                 if (busy) {
-                    const int key0 = (w.blk + (two ? s : 2 * s + grp)) * BK;
-                    const bool mask = key0 + BK > len;  // the block reaches the tree's slots
-                    // S is read twice, 64 columns at a time: kept whole it spills (128 values a
-                    // thread), and with nearly all of L1 given to shared memory a spill goes to L2
-                    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                    uint32_t x[2][32];
+                    tmem_ld_32x32b_x32(s_col + h * HK, x[0]);
+                    tmem_ld_32x32b_x32(s_col + h * HK + 32, x[1]);
+                    tmem_ld_wait();
+                    if (key0 + HK > len) hide(x, way, key0, len);  // the half reaches the tree's slots
+                    float mx[4];
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        uint32_t x[2][32];
-                        tmem_ld_32x32b_x32(s_col + h * 64, x[0]);
-                        tmem_ld_32x32b_x32(s_col + h * 64 + 32, x[1]);
-                        tmem_ld_wait();
-                        if (mask) hide64(x, way, key0 + h * 64, len);
+                    for (int q = 0; q < 4; ++q) {
+                        mx[q] = __uint_as_float(x[q >> 1][(q & 1) * 16]);
 #pragma unroll
-                        for (int c = 0; c < 64; ++c)
-                            mx[c & 3] = fmaxf(mx[c & 3], __uint_as_float(x[c >> 5][c & 31]));
+                        for (int c = 1; c < 15; c += 2)
+                            mx[q] = max3(mx[q], __uint_as_float(x[q >> 1][(q & 1) * 16 + c]),
+                                         __uint_as_float(x[q >> 1][(q & 1) * 16 + c + 1]));
+                        mx[q] = fmaxf(mx[q], __uint_as_float(x[q >> 1][(q & 1) * 16 + 15]));
                     }
                     const float m_blk = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2;
                     const bool resc = m_blk > m_use + kRescaleLog2;
-                    const float m_new = resc ? m_blk : m_use;
-                    const float alpha = resc ? exp2f(m_use - m_new) : 1.0f;
-                    const float neg_m = m_new == -INFINITY ? 0.0f : -m_new;
-                    if (s > 0 && __any_sync(0xffffffffu, resc)) {
-                        // the group's P.V so far are done (S of this step was issued after them)
+                    if (__any_sync(0xffffffffu, resc)) {
+                        const float m_new = resc ? m_blk : m_use;
+                        const float alpha = resc ? exp2f(m_use - m_new) : 1.0f;
+                        m_use = m_new;
+                        l *= alpha;
+                        if (n > 0) {  // O holds the halves before: they are added once the last P.V is done
+                            if (!__all_sync(0xffffffffu, mbar_wait(pv_done, (halves - 1) & 1u, status, abort_flag))) {
+                                ok = false;
+                                break;
+                            }
+                            tc_fence_after();
 #pragma unroll 1
-                        for (int q = 0; q < 4; ++q) {
-                            uint32_t o[32];
-                            const uint32_t oc = tmem + lane_base + TM_O + grp * D + q * 32;
-                            tmem_ld_32x32b_x32(oc, o);
-                            tmem_ld_wait();
+                            for (int q = 0; q < 8; ++q) {
+                                uint32_t o[16];
+                                const uint32_t oc = tmem + lane_base + TM_O + grp * D + q * 16;
+                                tmem_ld_32x32b_x16(oc, o);
+                                tmem_ld_wait();
 #pragma unroll
-                            for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * alpha);
-                            tmem_st_32x32b_x32(oc, o);
+                                for (int c = 0; c < 16; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * alpha);
+                                tmem_st_32x32b_x16(oc, o);
+                            }
                         }
                     }
-                    m_use = m_new;
-                    float sm[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        uint32_t x[2][32];
-                        tmem_ld_32x32b_x32(s_col + h * 64, x[0]);
-                        tmem_ld_32x32b_x32(s_col + h * 64 + 32, x[1]);
-                        tmem_ld_wait();
-                        if (mask) hide64(x, way, key0 + h * 64, len);
-                        // P over columns of S already read
-                        if (mask)
-                            exp64<true>(x, a.scale_log2, neg_m, sm, s_col + h * 32);
-                        else
-                            exp64<false>(x, a.scale_log2, neg_m, sm, s_col + h * 32);
-                    }
+                    // P lies over this half's S, whose every column has been read
+                    l += exp_half(x, a.scale_log2, m_use == -INFINITY ? 0.0f : -m_use, s_col + h * HK);
                     tmem_st_wait();
-                    l = l * alpha + ((sm[0] + sm[1]) + (sm[2] + sm[3]));
                 }
-                const int j = two ? s : 2 * s + grp, at = (w.blk + j) * BK - len;
-                if (at + BK > 0 && (!two || grp == 0)) {
-                    // slots that no node holds may contain anything: their values become zeros,
-                    // a thread per key
-                    const int vs = (c0 + j) % a.nv, slot = at + i;
-                    if (!__all_sync(0xffffffffu, mbar_wait(smem_addr(&bars->v_full[vs]), (uint32_t)((c0 + j) / a.nv) & 1u,
-                                                           status, abort_flag))) {
+                if (key0 + HK > len) {
+                    // slots that no node holds may contain anything: their values become zeros, two
+                    // threads per key (with two tiles both groups write the same zeros)
+                    const int slot = key0 + (i & 63) - len;
+                    if (!__all_sync(0xffffffffu,
+                                    mbar_wait(smem_addr(&bars->v_full[v.slot]), v.phase, status, abort_flag))) {
                         ok = false;
                         break;
                     }
                     if (slot >= a.T || (slot >= 0 && a.parents && tree_way(par, slot) == 0)) {
-                        const uint32_t v = smem_addr(sV + vs * V_BYTES) + i * 128;
+                        const uint32_t vrow = smem_addr(sV + v.slot * V_BYTES) + (i >> 6) * V_CHUNK + (h * HK + (i & 63)) * 128;
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            st_shared_v4(v + ((e + lane) & 7) * 16, make_uint4(0, 0, 0, 0));
-                            st_shared_v4(v + V_CHUNK + ((e + lane) & 7) * 16, make_uint4(0, 0, 0, 0));
-                        }
+                        for (int e = 0; e < 8; ++e) st_shared_v4(vrow + ((e + lane) & 7) * 16, make_uint4(0, 0, 0, 0));
                     }
                     fence_proxy_async_smem();
                 }
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(smem_addr(&bars->p_full[grp]));
+                if (lane == 0) mbar_arrive(p_full + h * 8);
+                if (h) v.next(two ? 1 : 2, a.nv);
             }
             if (!ok) break;
-            c0 += w.n;
+            for (int j = 0; j < w.n; ++j) v0.next(1, a.nv);
             if (!__all_sync(0xffffffffu,
                             mbar_wait(smem_addr(&bars->o_full), (uint32_t)piece & 1u, status, abort_flag))) {
                 ok = false;
