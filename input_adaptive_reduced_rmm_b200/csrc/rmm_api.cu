@@ -735,9 +735,9 @@ bool attn_tree_sizes_ok(int B, int Hq, int Hkv, int T, int ldL) {
     return B >= 1 && Hq >= 1 && Hkv >= 1 && T >= 1 && Hq % Hkv == 0 && ldL >= T && ldL % 8 == 0;
 }
 
-bool attn_tree_supported(int B, int Hq, int T, int d, const rmm_options& o) {
+bool attn_tree_supported(int B, int Hq, int T, int ldL, int d, const rmm_options& o) {
     // (rows of queries and of K^T are int coordinates of the tensor maps)
-    return d == 128 && T <= kTreeMax && Hq <= kTreeMaxHeads && B <= kTreeMaxBatch && (int64_t)B * Hq < (1 << 24) &&
+    return d == 128 && T <= kTreeMax && ldL <= (1 << 24) && Hq <= kTreeMaxHeads && B <= kTreeMaxBatch && (int64_t)B * Hq < (1 << 24) &&
            !o.attn_per_query_head && o.attn_path == 0;
 }
 
@@ -745,7 +745,7 @@ bool attn_tree_supported(int B, int Hq, int T, int d, const rmm_options& o) {
 
 size_t rmm_attn_tree_workspace_bytes(int B, int Hq, int Hkv, int T, int ldL, int d, const rmm_options* options) {
     if (!attn_tree_sizes_ok(B, Hq, Hkv, T, ldL) || !opts_valid(options) ||
-        !attn_tree_supported(B, Hq, T, d, opts_or_default(options)))
+        !attn_tree_supported(B, Hq, T, ldL, d, opts_or_default(options)))
         return 0;
     return kStatusBytes + align_up((size_t)B * Hkv * d * sizeof(int32_t), kAlign) +
            align_up(attn_tree_partial_bytes(B, Hq, Hkv, T, ldL, num_sms_current()), kAlign);
@@ -759,7 +759,7 @@ rmm_status rmm_attn_tree(const void* Q, const void* Kt, const void* V, const int
         return RMM_ERR_INVALID_ARG;
     if (!aligned16(Q) || !aligned16(Kt) || !aligned16(V) || !aligned16(O)) return RMM_ERR_INVALID_ARG;
     if (!(scale > 0.0f) || !isfinite(scale)) return RMM_ERR_INVALID_ARG;
-    if (!attn_tree_supported(B, Hq, T, d, opts_or_default(options))) return RMM_ERR_UNSUPPORTED;
+    if (!attn_tree_supported(B, Hq, T, ldL, d, opts_or_default(options))) return RMM_ERR_UNSUPPORTED;
     const int k = rmm_k_for(d, r);
     if (k < 1) return RMM_ERR_INVALID_ARG;
     const int sms = num_sms_current();
@@ -772,15 +772,14 @@ rmm_status rmm_attn_tree(const void* Q, const void* Kt, const void* V, const int
     CUtensorMap qm, km, vm;
     try {
         if (!tiled_map(Q, (uint64_t)B * Hq * T, d, d, 128, &qm) ||
-            !(k == d ? tiled_map_3d(Kt, ldL, d, planes, ldL, (uint64_t)d * ldL, 128, &km)
-                     : row_gather_map(Kt, planes * d, ldL, ldL, &km)) ||
+            !tiled_map_3d(Kt, ldL, d, planes, ldL, (uint64_t)d * ldL, 128, &km) ||
             !tiled_map_3d(V, d, ldL, planes, d, (uint64_t)d * ldL, 128, &vm))
             return RMM_ERR_CUDA;
     } catch (...) {  // the maps' cache is out of memory
         return RMM_ERR_CUDA;
     }
-    return cuda_status(launch_attn_tree(qm, km, vm, static_cast<const uint16_t*>(Q), B, Hq, Hkv, T, ldL, k, scale, lens,
-                                        parents, static_cast<uint16_t*>(O),
+    return cuda_status(launch_attn_tree(qm, km, vm, static_cast<const uint16_t*>(Q), static_cast<const uint16_t*>(Kt), B,
+                                        Hq, Hkv, T, ldL, k, scale, lens, parents, static_cast<uint16_t*>(O),
                                         idx_out ? idx_out : reinterpret_cast<int32_t*>(ws + kStatusBytes),
                                         idx_out != nullptr, ws + kStatusBytes + idx_bytes, reinterpret_cast<int*>(ws),
                                         sms, static_cast<cudaStream_t>(stream)));

@@ -32,9 +32,9 @@
 //              the query operand at the start of a unit, its output at the end
 //   warps 8, 9 MMA, a thread for each group: S = Q_S K_S^T for the group's next step
 //              as soon as its P.V is done, P.V (A from TMEM) as soon as its P is written
-//   warp 10    TMA: key and value blocks through two rings, running ahead over
-//              units.  With every dim kept the key block is two tile copies of
-//              the d-major cache; else the kept rows come by tile::gather4.
+//   warp 10    key and value blocks through two rings, running ahead over units:
+//              tile copies, or (fewer dims kept) the kept rows of K^T gathered
+//              together with warp 11
 //
 // Operands in shared memory are 128-byte swizzled: K and V MN-major as the
 // caches lay them out, Q K-major (a tile copy) or, gathered, MN-major.  TMEM
@@ -80,7 +80,7 @@ struct __align__(8) TreeBars {
 };
 
 struct TreeArgs {
-    const uint16_t* Q;
+    const uint16_t *Q, *Kt;
     const int32_t *lens, *parents;
     int32_t* idx;  // kept sets [B * Hkv * k]
     uint16_t* O;
@@ -186,6 +186,36 @@ __device__ __forceinline__ float exp_half(const uint32_t (&x)[2][32], float scal
     return (sum[0] + sum[1]) + (sum[2] + sum[3]);
 }
 
+// umma_f16, umma_f16_tmem_a and umma_commit by one thread of a converged warp (the
+// same one each time).
+__device__ __forceinline__ void umma_f16_elect(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                               uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+__device__ __forceinline__ void umma_f16_tmem_a_elect(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                                                      uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+__device__ __forceinline__ void umma_commit_elect(uint32_t bar) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar)
+        : "memory");
+}
+
 // kAll: every head dimension kept (Q a tile copy, K-major; key blocks tile copies).
 template <bool kAll>
 __global__ void __launch_bounds__(kThreadsTree, 1)
@@ -211,7 +241,7 @@ __global__ void __launch_bounds__(kThreadsTree, 1)
         mbar_init(smem_addr(&bars->o_full), 2);
         mbar_init(smem_addr(&bars->drain), 2);
         for (int s = 0; s < kMaxStages; ++s) {
-            mbar_init(smem_addr(&bars->k_full[s]), 1);
+            mbar_init(smem_addr(&bars->k_full[s]), kAll ? 1 : 64);  // a tile's bytes, or 64 threads' copies
             mbar_init(smem_addr(&bars->k_empty[s]), users);
             mbar_init(smem_addr(&bars->v_full[s]), 1);
             mbar_init(smem_addr(&bars->v_empty[s]), users);
@@ -285,151 +315,166 @@ __global__ void __launch_bounds__(kThreadsTree, 1)
     const uint32_t tmem = bars->tmem_base;
 
     Share w;
-    if (warp == kTmaWarp) {
+    if (warp == kTmaWarp || (!kAll && warp == kTmaWarp + 1)) {
         // ------------------------------------------------------------ key and value blocks
-        int c = 0;  // blocks issued
+        // Every dim kept: one thread copies tiles.  Else both warps gather the kept rows of K^T
+        // with 16-byte copies, and one thread copies the value tiles.
+        const int part = warp - kTmaWarp;
+        int c = 0, c_keys = 0;  // blocks issued, and key blocks (one more after an abort)
         Ring k, v;
         bool ok = true;
-        const int oob = a.B * a.Hkv * D;  // a row outside the key map: reads as zeros
         for (bool more = w.next(a, bars, true); ok && more; more = w.next(a, bars, false)) {
             const int plane = w.b * a.Hkv + w.u / a.nrp;
-            int r0 = 0, r1 = 0, r2 = 0, r3 = 0;
-            if (!kAll && lane * 4 < kp) {  // this lane's four kept rows of K^T
-                const int32_t* S = a.idx + (size_t)plane * a.k + lane * 4;
-                r0 = lane * 4 + 0 < a.k ? plane * D + S[0] : oob;
-                r1 = lane * 4 + 1 < a.k ? plane * D + S[1] : oob;
-                r2 = lane * 4 + 2 < a.k ? plane * D + S[2] : oob;
-                r3 = lane * 4 + 3 < a.k ? plane * D + S[3] : oob;
+            // Half-warps take every fourth kept row, a lane 8 keys of it: the rows' places in the
+            // d-major cache.  The padding repeats a kept row (its query values are zeros).
+            const int c16 = lane & 15, row = part * 2 + (lane >> 4);
+            uint32_t at[32];
+            if (!kAll) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    if (4 * i < kp) at[i] = (uint32_t)a.idx[(size_t)plane * a.k + (4 * i + row < a.k ? 4 * i + row : 0)] * a.ldL;
             }
+            const uint16_t* Kg = a.Kt + (size_t)plane * D * a.ldL + c16 * 8;
             for (int j = 0; j < w.n; ++j, ++c) {
                 const int key0 = (w.blk + j) * BK;
-                if (!__all_sync(0xffffffffu, mbar_wait(smem_addr(&bars->k_empty[k.slot]), k.phase ^ 1u, status, abort_flag))) {
+                if (!__all_sync(0xffffffffu,
+                                mbar_wait(smem_addr(&bars->k_empty[k.slot]), k.phase ^ 1u, status, abort_flag))) {
                     ok = false;
                     break;
                 }
                 const uint32_t kb = smem_addr(sK + k.slot * QK_BYTES), kf = smem_addr(&bars->k_full[k.slot]);
-                if (lane == 0) mbar_arrive_expect_tx(kf, QK_BYTES);
-                __syncwarp();
                 if (kAll) {
                     if (lane == 0) {
+                        mbar_arrive_expect_tx(kf, QK_BYTES);
                         tma_load_3d(kb, &kmap, kf, key0, 0, plane);
                         tma_load_3d(kb + D * 128, &kmap, kf, key0 + 64, 0, plane);
                     }
-                } else if (lane * 4 < kp) {
-                    tma_gather4(kb + lane * 512, &kmap, kf, key0, r0, r1, r2, r3);
-                    tma_gather4(kb + kp * 128 + lane * 512, &kmap, kf, key0 + 64, r0, r1, r2, r3);
+                } else {
+                    // row 4 i + row lies at 512 i + 128 row of its 64-key chunk, its 16-byte pieces
+                    // permuted by (row + 4 i) mod 8
+                    const uint32_t even = kb + swz(row, c16, kp * 128), odd = kb + swz(row + 4, c16, kp * 128) - 512;
+                    const uint32_t bytes = key0 + c16 * 8 < a.ldL ? 16u : 0u;
+                    const uint16_t* src = bytes ? Kg + key0 : Kg;
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        if (4 * i < kp) cp_async_16((i & 1 ? odd : even) + 512 * i, src + at[i], bytes);
+                    cp_async_arrive_noinc(kf);
                 }
-                const bool got = mbar_wait(smem_addr(&bars->v_empty[v.slot]), v.phase ^ 1u, status, abort_flag);
-                if (!__all_sync(0xffffffffu, got)) {
-                    // this block's keys are on their way, its values are not
-                    if (lane == 0) {
-                        volatile int no_abort = 0;
-                        mbar_wait(kf, k.phase, status, &no_abort);
-                    }
-                    ok = false;
-                    break;
-                }
-                if (lane == 0) {
-                    const uint32_t vb = smem_addr(sV + v.slot * V_BYTES), vf = smem_addr(&bars->v_full[v.slot]);
-                    mbar_arrive_expect_tx(vf, V_BYTES);
-                    tma_load_3d(vb, &vmap, vf, 0, key0, plane);
-                    tma_load_3d(vb + V_CHUNK, &vmap, vf, 64, key0, plane);
-                }
-                __syncwarp();
+                ++c_keys;
                 k.next(1, a.nk);
-                v.next(1, a.nv);
+                if (part == 0) {
+                    if (!__all_sync(0xffffffffu,
+                                    mbar_wait(smem_addr(&bars->v_empty[v.slot]), v.phase ^ 1u, status, abort_flag))) {
+                        ok = false;
+                        break;
+                    }
+                    if (lane == 0) {
+                        const uint32_t vb = smem_addr(sV + v.slot * V_BYTES), vf = smem_addr(&bars->v_full[v.slot]);
+                        mbar_arrive_expect_tx(vf, V_BYTES);
+                        tma_load_3d(vb, &vmap, vf, 0, key0, plane);
+                        tma_load_3d(vb + V_CHUNK, &vmap, vf, 64, key0, plane);
+                    }
+                    v.next(1, a.nv);
+                }
             }
         }
         // no copy may still be landing when the CTA leaves (after an abort; else all were consumed)
-        if (lane == 0) {
+        if (!kAll) cp_async_wait_all();
+        if (part == 0 && lane == 0) {
             volatile int no_abort = 0;
-            for (int j = max(0, c - a.nk); j < c; ++j)
-                mbar_wait(smem_addr(&bars->k_full[j % a.nk]), (uint32_t)(j / a.nk) & 1u, status, &no_abort);
+            if (kAll)
+                for (int j = max(0, c_keys - a.nk); j < c_keys; ++j)
+                    mbar_wait(smem_addr(&bars->k_full[j % a.nk]), (uint32_t)(j / a.nk) & 1u, status, &no_abort);
             for (int j = max(0, c - a.nv); j < c; ++j)
                 mbar_wait(smem_addr(&bars->v_full[j % a.nv]), (uint32_t)(j / a.nv) & 1u, status, &no_abort);
         }
         __syncwarp();
     } else if (warp == kMmaWarp || warp == kMmaWarp + 1) {
-        // ------------------------------------------------------------ MMA issuers: a thread per group
-        if (lane == 0) {
-            const int g = warp - kMmaWarp;
-            const uint32_t idesc_s = idesc_bf16_f32(BM, HK, kAll ? 0 : 1, 1);
-            const uint32_t idesc_pv = idesc_bf16_f32(BM, D, 0, 1);
-            const uint64_t qd0 = smem_desc_sw128(smem_addr(sQ), kAll ? 16 : kp * 128, 1024);
-            const uint64_t kd0 = smem_desc_sw128(smem_addr(sK), kp * 128, 1024);
-            const uint64_t vd0 = smem_desc_sw128(smem_addr(sV), V_CHUNK, 1024);
-            const uint32_t s_tm = tmem + g * BK, o_tm = tmem + TM_O + g * D;
-            const uint32_t s_full = smem_addr(&bars->s_full[g][0]), p_full = smem_addr(&bars->p_full[g][0]);
-            const uint32_t pv_done = smem_addr(&bars->pv_done[g]);
-            const int k_steps = kp / 16;
-            Ring k0, v0;              // the piece's first block
-            uint32_t pv = 0;          // P.V products issued (two per block)
-            int piece = 0;
-            bool ok = true;
-            for (bool more = w.next(a, bars, true); ok && more; more = w.next(a, bars, false), ++piece) {
-                // with two row tiles every block is this group's, with one every second
-                const bool two = 2 * (w.u % a.nrp) + 1 < a.nrt;
-                const int by = two ? 1 : 2, steps = two ? w.n : (w.n + 1 - g) / 2;
-                const int releases = two ? 1 : users;  // the group alone releases a block of one tile
-                const uint64_t qd = qd0 + (uint64_t)((two ? g : 0) * (QK_BYTES / 16));  // descriptors count 16 bytes
-                Ring k = k0, v = v0;
-                if (!two && g == 1) k.next(1, a.nk), v.next(1, a.nv);
-                ok = mbar_wait(smem_addr(&bars->q_full), (uint32_t)piece & 1u, status, abort_flag);
-                fence_proxy_async_smem();  // a gathered query operand, written by the softmax warps
-                // halves of the group's blocks: P.V of one, then S of the same half of the next block,
-                // while the softmax works on the other half
-                for (int n = -2; ok && n < 2 * steps; ++n) {
-                    const int h = n & 1;
-                    if (n >= 0) {
-                        ok = (h || mbar_wait(smem_addr(&bars->v_full[v.slot]), v.phase, status, abort_flag)) &&
-                             mbar_wait(p_full + h * 8, (pv >> 1) & 1u, status, abort_flag);
-                        if (!ok) break;
-                        tc_fence_after();
-                        const uint64_t vd = vd0 + (uint64_t)(v.slot * (V_BYTES / 16) + h * (HK * 8));
+        // ------------------------------------------------------------ MMA issuers: a warp per group
+        // The warp stays together and every instruction elects its thread, so that descriptors
+        // are computed once for the warp: issued from a branch of one thread, a product took
+        // about 110 cycles whatever its size.
+        const int g = warp - kMmaWarp;
+        const uint32_t idesc_s = idesc_bf16_f32(BM, HK, kAll ? 0 : 1, 1);
+        const uint32_t idesc_pv = idesc_bf16_f32(BM, D, 0, 1);
+        const uint64_t qd0 = smem_desc_sw128(smem_addr(sQ), kAll ? 16 : kp * 128, 1024);
+        const uint64_t kd0 = smem_desc_sw128(smem_addr(sK), kp * 128, 1024);
+        const uint64_t vd0 = smem_desc_sw128(smem_addr(sV), V_CHUNK, 1024);
+        const uint32_t s_tm = tmem + g * BK, o_tm = tmem + TM_O + g * D;
+        const uint32_t s_full = smem_addr(&bars->s_full[g][0]), p_full = smem_addr(&bars->p_full[g][0]);
+        const uint32_t pv_done = smem_addr(&bars->pv_done[g]);
+        const int k_steps = kp / 16;
+        auto wait = [&](uint32_t bar, uint32_t phase) -> bool {
+            return __all_sync(0xffffffffu, mbar_wait(bar, phase, status, abort_flag));
+        };
+        Ring k0, v0;              // the piece's first block
+        uint32_t pv = 0;          // P.V products issued (two per block)
+        int piece = 0;
+        bool ok = true;
+        for (bool more = w.next(a, bars, true); ok && more; more = w.next(a, bars, false), ++piece) {
+            // with two row tiles every block is this group's, with one every second
+            const bool two = 2 * (w.u % a.nrp) + 1 < a.nrt;
+            const int by = two ? 1 : 2, steps = two ? w.n : (w.n + 1 - g) / 2;
+            const int releases = two ? 1 : users;  // the group alone releases a block of one tile
+            const uint64_t qd = qd0 + (uint64_t)((two ? g : 0) * (QK_BYTES / 16));  // descriptors count 16 bytes
+            Ring k = k0, v = v0;
+            if (!two && g == 1) k.next(1, a.nk), v.next(1, a.nv);
+            ok = wait(smem_addr(&bars->q_full), (uint32_t)piece & 1u);
+            fence_proxy_async_smem();  // a gathered query operand, written by the softmax warps
+            // halves of the group's blocks: P.V of one, then S of the same half of the next block,
+            // while the softmax works on the other half
+            for (int n = -2; ok && n < 2 * steps; ++n) {
+                const int h = n & 1;
+                if (n >= 0) {
+                    ok = (h || wait(smem_addr(&bars->v_full[v.slot]), v.phase)) && wait(p_full + h * 8, (pv >> 1) & 1u);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint64_t vd = vd0 + (uint64_t)(v.slot * (V_BYTES / 16) + h * (HK * 8));
 #pragma unroll
-                        for (int kk = 0; kk < HK / 16; ++kk)
-                            umma_f16_tmem_a(o_tm, s_tm + h * HK + kk * 8, vd + kk * 128, idesc_pv,
-                                            kk > 0 || n > 0 ? 1u : 0u);
-                        umma_commit(pv_done);
-                        if (h) {
-                            for (int r = 0; r < releases; ++r) umma_commit(smem_addr(&bars->v_empty[v.slot]));
-                            v.next(by, a.nv);
-                        }
-                        ++pv;
+                    for (int kk = 0; kk < HK / 16; ++kk)
+                        umma_f16_tmem_a_elect(o_tm, s_tm + h * HK + kk * 8, vd + kk * 128, idesc_pv,
+                                              kk > 0 || n > 0 ? 1u : 0u);
+                    umma_commit_elect(pv_done);
+                    if (h) {
+                        for (int r = 0; r < releases; ++r) umma_commit_elect(smem_addr(&bars->v_empty[v.slot]));
+                        v.next(by, a.nv);
                     }
-                    if (n + 2 < 2 * steps) {
-                        ok = h || mbar_wait(smem_addr(&bars->k_full[k.slot]), k.phase, status, abort_flag);
-                        // the P.V just issued reads P, which lies over this half's S
-                        if (ok && n >= 0) ok = mbar_wait(pv_done, (pv - 1) & 1u, status, abort_flag);
-                        if (!ok) break;
-                        tc_fence_after();
-                        const uint64_t kd = kd0 + (uint64_t)(k.slot * (QK_BYTES / 16) + h * (kp * 8));
-                        if (kAll) {
+                    ++pv;
+                }
+                if (n + 2 < 2 * steps) {
+                    ok = h || wait(smem_addr(&bars->k_full[k.slot]), k.phase);
+                    // the P.V just issued reads P, which lies over this half's S
+                    if (ok && n >= 0) ok = wait(pv_done, (pv - 1) & 1u);
+                    if (!ok) break;
+                    if (!kAll) fence_proxy_async_smem();  // copied keys, read by the tensor cores
+                    tc_fence_after();
+                    const uint64_t kd = kd0 + (uint64_t)(k.slot * (QK_BYTES / 16) + h * (kp * 8));
+                    if (kAll) {
 #pragma unroll
-                            for (int kk = 0; kk < D / 16; ++kk)
-                                umma_f16(s_tm + h * HK, qd + (kk >> 2) * (BM * 8) + (kk & 3) * 2, kd + kk * 128, idesc_s,
-                                         kk > 0 ? 1u : 0u);
-                        } else {
-                            uint64_t q1 = qd, k1 = kd;
+                        for (int kk = 0; kk < D / 16; ++kk)
+                            umma_f16_elect(s_tm + h * HK, qd + (kk >> 2) * (BM * 8) + (kk & 3) * 2, kd + kk * 128,
+                                           idesc_s, kk > 0 ? 1u : 0u);
+                    } else {
+                        uint64_t q1 = qd, k1 = kd;
 #pragma unroll 1
-                            for (int kk = 0; kk < k_steps; ++kk, q1 += 128, k1 += 128)
-                                umma_f16(s_tm + h * HK, q1, k1, idesc_s, kk > 0 ? 1u : 0u);
-                        }
-                        umma_commit(s_full + h * 8);
-                        if (h) {
-                            for (int r = 0; r < releases; ++r) umma_commit(smem_addr(&bars->k_empty[k.slot]));
-                            k.next(by, a.nk);
-                        }
+                        for (int kk = 0; kk < k_steps; ++kk, q1 += 128, k1 += 128)
+                            umma_f16_elect(s_tm + h * HK, q1, k1, idesc_s, kk > 0 ? 1u : 0u);
+                    }
+                    umma_commit_elect(s_full + h * 8);
+                    if (h) {
+                        for (int r = 0; r < releases; ++r) umma_commit_elect(smem_addr(&bars->k_empty[k.slot]));
+                        k.next(by, a.nk);
                     }
                 }
-                if (ok) umma_commit(smem_addr(&bars->o_full));
-                for (int j = 0; j < w.n; ++j) k0.next(1, a.nk), v0.next(1, a.nv);
             }
-            umma_commit(smem_addr(&bars->drain));
-            // issued MMAs finish on their own; TMEM is not freed under them
-            volatile int no_abort = 0;
-            mbar_wait(smem_addr(&bars->drain), 0, status, &no_abort);
+            if (ok) umma_commit_elect(smem_addr(&bars->o_full));
+            for (int j = 0; j < w.n; ++j) k0.next(1, a.nk), v0.next(1, a.nv);
         }
+        __syncwarp();
+        umma_commit_elect(smem_addr(&bars->drain));
+        // issued MMAs finish on their own; TMEM is not freed under them
+        volatile int no_abort = 0;
+        mbar_wait(smem_addr(&bars->drain), 0, status, &no_abort);
         __syncwarp();
     } else if (warp < kMmaWarp) {
         // ------------------------------------------------------------ softmax, query operand, output
@@ -819,12 +864,13 @@ size_t attn_tree_partial_bytes(int B, int Hq, int Hkv, int T, int ldL, int num_s
 }
 
 cudaError_t launch_attn_tree(const CUtensorMap& qmap, const CUtensorMap& kmap, const CUtensorMap& vmap,
-                             const uint16_t* Q, int B, int Hq, int Hkv, int T, int ldL, int k, float scale,
+                             const uint16_t* Q, const uint16_t* Kt, int B, int Hq, int Hkv, int T, int ldL, int k, float scale,
                              const int32_t* lens, const int32_t* parents, uint16_t* O, int32_t* idx, int want_idx,
                              void* partials, int* status, int num_sms, cudaStream_t stream) {
     const TreePlan p = tree_plan(B, Hq, Hkv, T, ldL, num_sms);
     TreeArgs a{};
     a.Q = Q;
+    a.Kt = Kt;
     a.lens = lens;
     a.parents = parents;
     a.identity = k == D;

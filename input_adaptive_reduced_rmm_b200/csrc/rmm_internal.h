@@ -195,12 +195,12 @@ cudaError_t launch_qkv_rope(const uint16_t* Yq, const uint16_t* Yk, const uint16
 // Bytes of split partials for these sizes.
 size_t attn_tree_partial_bytes(int B, int Hq, int Hkv, int T, int ldL, int num_sms);
 // qmap: Q as rows of 128 dims, box 64 x 128; kmap: Kt as [plane][dim][key], box 64 keys x 128
-// dims (k == 128), or as rows (plane, dim) of ldL keys for tile::gather4; vmap: V as
+// dims; vmap: V as
 // [plane][key][dim], box 64 x 128.  idx: int32 [B * Hkv * k], written (with k == 128 only if want_idx).
 cudaError_t launch_attn_tree(const CUtensorMap& qmap, const CUtensorMap& kmap, const CUtensorMap& vmap,
-                             const uint16_t* Q, int B, int Hq, int Hkv, int T, int ldL, int k, float scale,
-                             const int32_t* lens, const int32_t* parents, uint16_t* O, int32_t* idx, int want_idx,
-                             void* partials, int* status, int num_sms, cudaStream_t stream);
+                             const uint16_t* Q, const uint16_t* Kt, int B, int Hq, int Hkv, int T, int ldL, int k,
+                             float scale, const int32_t* lens, const int32_t* parents, uint16_t* O, int32_t* idx,
+                             int want_idx, void* partials, int* status, int num_sms, cudaStream_t stream);
 constexpr int kSoftmaxMaxV = 262144;  // logits per row
 cudaError_t launch_softmax(const uint16_t* X, int rows, int V, int64_t ldx, float temperature, float* Y, int64_t ldy,
                            cudaStream_t stream);
