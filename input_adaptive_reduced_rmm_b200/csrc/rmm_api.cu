@@ -773,7 +773,7 @@ rmm_status rmm_attn_tree(const void* Q, const void* Kt, const void* V, const int
     try {
         if (!tiled_map(Q, (uint64_t)B * Hq * T, d, d, 128, &qm) ||
             !tiled_map_3d(Kt, ldL, d, planes, ldL, (uint64_t)d * ldL, 128, &km) ||
-            !tiled_map_3d(V, d, ldL, planes, d, (uint64_t)d * ldL, 128, &vm))
+            !tiled_map_3d(V, d, ldL, planes, d, (uint64_t)d * ldL, 64, &vm))
             return RMM_ERR_CUDA;
     } catch (...) {  // the maps' cache is out of memory
         return RMM_ERR_CUDA;

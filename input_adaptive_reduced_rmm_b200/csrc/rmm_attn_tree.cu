@@ -32,9 +32,9 @@
 //              the query operand at the start of a unit, its output at the end
 //   warps 8, 9 MMA, a thread for each group: S = Q_S K_S^T for the group's next step
 //              as soon as its P.V is done, P.V (A from TMEM) as soon as its P is written
-//   warp 10    key and value blocks through two rings, running ahead over units:
-//              tile copies, or (fewer dims kept) the kept rows of K^T gathered
-//              together with warp 11
+//   warp 10    key and value blocks by tile copies through two rings, running ahead
+//              over units
+//   12-15      (fewer dims kept) the kept rows of K^T gathered from the d-major cache
 //
 // Operands in shared memory are 128-byte swizzled: K and V MN-major as the
 // caches lay them out, Q K-major (a tile copy) or, gathered, MN-major.  TMEM
@@ -54,15 +54,15 @@ namespace {
 
 constexpr int D = 128;
 constexpr int BM = 128;  // rows per tile (= TMEM lanes)
-constexpr int BK = 128;  // keys per block
-constexpr int HK = 64;   // keys per half: the step of S, softmax and P.V
-constexpr int kMaxStages = 6;
+constexpr int BK = 64;   // keys per block: the step of S, softmax and P.V
+constexpr int kMaxStages = 8;
 constexpr int kSoftmaxThreads = 256;
 constexpr int kMmaWarp = 8, kTmaWarp = 10;  // MMA warps 8 and 9: one per group
-constexpr int kThreadsTree = 384;
-constexpr int V_CHUNK = BK * 128;  // 64 dims of a value block
+constexpr int kGatherWarp = 12, kGatherWarps = 4;  // key rows, when not every dim is kept
+constexpr int tree_threads(bool all) { return 32 * (all ? kGatherWarp : kGatherWarp + kGatherWarps); }
+constexpr int V_CHUNK = BK * 128;  // 64 dims of a value block (bytes)
 constexpr int V_BYTES = 2 * V_CHUNK;
-constexpr uint32_t TM_O = 256;  // S of group a at 128 a, O of group a at 256 + 128 a
+constexpr uint32_t TM_O = 256;  // S of group a at 128 a (two buffers), O of group a at 256 + 128 a
 constexpr float kRescaleLog2 = 8.0f;
 constexpr int kSmemMax = 232448;  // 227 KB
 
@@ -70,7 +70,7 @@ struct __align__(8) TreeBars {
     uint64_t q_full, o_full, drain;
     uint64_t k_full[kMaxStages], k_empty[kMaxStages];
     uint64_t v_full[kMaxStages], v_empty[kMaxStages];
-    uint64_t s_full[2][2], p_full[2][2];  // [group][half of the block]
+    uint64_t s_full[2][2], p_full[2][2];  // [group][buffer]
     uint64_t pv_done[2];
     uint64_t meet;  // all softmax warps
     long long pos;  // the CTA's share: first block, and how many
@@ -168,7 +168,7 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
 
 // p = 2^(x scale - m) for 64 logits of a row, their sum, and P (bf16) to the 32
 // columns at pcol.
-__device__ __forceinline__ float exp_half(const uint32_t (&x)[2][32], float scale_log2, float neg_m, uint32_t pcol) {
+__device__ __forceinline__ float exp_block(const uint32_t (&x)[2][32], float scale_log2, float neg_m, uint32_t pcol) {
     float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
@@ -218,18 +218,18 @@ __device__ __forceinline__ void umma_commit_elect(uint32_t bar) {
 
 // kAll: every head dimension kept (Q a tile copy, K-major; key blocks tile copies).
 template <bool kAll>
-__global__ void __launch_bounds__(kThreadsTree, 1)
+__global__ void __launch_bounds__(tree_threads(kAll), 1)
     attn_tree_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
                      const __grid_constant__ CUtensorMap vmap, const TreeArgs a) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~static_cast<uintptr_t>(1023));
     const int kp = kAll ? D : a.kp;
-    const int QK_BYTES = kp * 256;  // a query tile or a key block
+    const int Q_BYTES = kp * 256, K_BYTES = kp * 128;  // a query tile, a key block
     uint8_t* sV = smem;
     uint8_t* sK = sV + a.nv * V_BYTES;
-    uint8_t* sQ = sK + a.nk * QK_BYTES;
-    TreeBars* bars = reinterpret_cast<TreeBars*>(sQ + (a.nrt > 1 ? 2 : 1) * QK_BYTES);
+    uint8_t* sQ = sK + a.nk * K_BYTES;
+    TreeBars* bars = reinterpret_cast<TreeBars*>(sQ + (a.nrt > 1 ? 2 : 1) * Q_BYTES);
     int32_t* par = reinterpret_cast<int32_t*>(bars + 1);
     volatile int* abort_flag = &bars->abort_flag;
     int* status = a.status;
@@ -241,7 +241,7 @@ __global__ void __launch_bounds__(kThreadsTree, 1)
         mbar_init(smem_addr(&bars->o_full), 2);
         mbar_init(smem_addr(&bars->drain), 2);
         for (int s = 0; s < kMaxStages; ++s) {
-            mbar_init(smem_addr(&bars->k_full[s]), kAll ? 1 : 64);  // a tile's bytes, or 64 threads' copies
+            mbar_init(smem_addr(&bars->k_full[s]), kAll ? 1 : 32 * kGatherWarps);  // a tile's bytes, or the threads' copies
             mbar_init(smem_addr(&bars->k_empty[s]), users);
             mbar_init(smem_addr(&bars->v_full[s]), 1);
             mbar_init(smem_addr(&bars->v_empty[s]), users);
@@ -315,178 +315,20 @@ __global__ void __launch_bounds__(kThreadsTree, 1)
     const uint32_t tmem = bars->tmem_base;
 
     Share w;
-    if (warp == kTmaWarp || (!kAll && warp == kTmaWarp + 1)) {
-        // ------------------------------------------------------------ key and value blocks
-        // Every dim kept: one thread copies tiles.  Else both warps gather the kept rows of K^T
-        // with 16-byte copies, and one thread copies the value tiles.
-        const int part = warp - kTmaWarp;
-        int c = 0, c_keys = 0;  // blocks issued, and key blocks (one more after an abort)
-        Ring k, v;
-        bool ok = true;
-        for (bool more = w.next(a, bars, true); ok && more; more = w.next(a, bars, false)) {
-            const int plane = w.b * a.Hkv + w.u / a.nrp;
-            // Half-warps take every fourth kept row, a lane 8 keys of it: the rows' places in the
-            // d-major cache.  The padding repeats a kept row (its query values are zeros).
-            const int c16 = lane & 15, row = part * 2 + (lane >> 4);
-            uint32_t at[32];
-            if (!kAll) {
-#pragma unroll
-                for (int i = 0; i < 32; ++i)
-                    if (4 * i < kp) at[i] = (uint32_t)a.idx[(size_t)plane * a.k + (4 * i + row < a.k ? 4 * i + row : 0)] * a.ldL;
-            }
-            const uint16_t* Kg = a.Kt + (size_t)plane * D * a.ldL + c16 * 8;
-            for (int j = 0; j < w.n; ++j, ++c) {
-                const int key0 = (w.blk + j) * BK;
-                if (!__all_sync(0xffffffffu,
-                                mbar_wait(smem_addr(&bars->k_empty[k.slot]), k.phase ^ 1u, status, abort_flag))) {
-                    ok = false;
-                    break;
-                }
-                const uint32_t kb = smem_addr(sK + k.slot * QK_BYTES), kf = smem_addr(&bars->k_full[k.slot]);
-                if (kAll) {
-                    if (lane == 0) {
-                        mbar_arrive_expect_tx(kf, QK_BYTES);
-                        tma_load_3d(kb, &kmap, kf, key0, 0, plane);
-                        tma_load_3d(kb + D * 128, &kmap, kf, key0 + 64, 0, plane);
-                    }
-                } else {
-                    // row 4 i + row lies at 512 i + 128 row of its 64-key chunk, its 16-byte pieces
-                    // permuted by (row + 4 i) mod 8
-                    const uint32_t even = kb + swz(row, c16, kp * 128), odd = kb + swz(row + 4, c16, kp * 128) - 512;
-                    const uint32_t bytes = key0 + c16 * 8 < a.ldL ? 16u : 0u;
-                    const uint16_t* src = bytes ? Kg + key0 : Kg;
-#pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        if (4 * i < kp) cp_async_16((i & 1 ? odd : even) + 512 * i, src + at[i], bytes);
-                    cp_async_arrive_noinc(kf);
-                }
-                ++c_keys;
-                k.next(1, a.nk);
-                if (part == 0) {
-                    if (!__all_sync(0xffffffffu,
-                                    mbar_wait(smem_addr(&bars->v_empty[v.slot]), v.phase ^ 1u, status, abort_flag))) {
-                        ok = false;
-                        break;
-                    }
-                    if (lane == 0) {
-                        const uint32_t vb = smem_addr(sV + v.slot * V_BYTES), vf = smem_addr(&bars->v_full[v.slot]);
-                        mbar_arrive_expect_tx(vf, V_BYTES);
-                        tma_load_3d(vb, &vmap, vf, 0, key0, plane);
-                        tma_load_3d(vb + V_CHUNK, &vmap, vf, 64, key0, plane);
-                    }
-                    v.next(1, a.nv);
-                }
-            }
-        }
-        // no copy may still be landing when the CTA leaves (after an abort; else all were consumed)
-        if (!kAll) cp_async_wait_all();
-        if (part == 0 && lane == 0) {
-            volatile int no_abort = 0;
-            if (kAll)
-                for (int j = max(0, c_keys - a.nk); j < c_keys; ++j)
-                    mbar_wait(smem_addr(&bars->k_full[j % a.nk]), (uint32_t)(j / a.nk) & 1u, status, &no_abort);
-            for (int j = max(0, c - a.nv); j < c; ++j)
-                mbar_wait(smem_addr(&bars->v_full[j % a.nv]), (uint32_t)(j / a.nv) & 1u, status, &no_abort);
-        }
-        __syncwarp();
-    } else if (warp == kMmaWarp || warp == kMmaWarp + 1) {
-        // ------------------------------------------------------------ MMA issuers: a warp per group
-        // The warp stays together and every instruction elects its thread, so that descriptors
-        // are computed once for the warp: issued from a branch of one thread, a product took
-        // about 110 cycles whatever its size.
-        const int g = warp - kMmaWarp;
-        const uint32_t idesc_s = idesc_bf16_f32(BM, HK, kAll ? 0 : 1, 1);
-        const uint32_t idesc_pv = idesc_bf16_f32(BM, D, 0, 1);
-        const uint64_t qd0 = smem_desc_sw128(smem_addr(sQ), kAll ? 16 : kp * 128, 1024);
-        const uint64_t kd0 = smem_desc_sw128(smem_addr(sK), kp * 128, 1024);
-        const uint64_t vd0 = smem_desc_sw128(smem_addr(sV), V_CHUNK, 1024);
-        const uint32_t s_tm = tmem + g * BK, o_tm = tmem + TM_O + g * D;
-        const uint32_t s_full = smem_addr(&bars->s_full[g][0]), p_full = smem_addr(&bars->p_full[g][0]);
-        const uint32_t pv_done = smem_addr(&bars->pv_done[g]);
-        const int k_steps = kp / 16;
-        auto wait = [&](uint32_t bar, uint32_t phase) -> bool {
-            return __all_sync(0xffffffffu, mbar_wait(bar, phase, status, abort_flag));
-        };
-        Ring k0, v0;              // the piece's first block
-        uint32_t pv = 0;          // P.V products issued (two per block)
-        int piece = 0;
-        bool ok = true;
-        for (bool more = w.next(a, bars, true); ok && more; more = w.next(a, bars, false), ++piece) {
-            // with two row tiles every block is this group's, with one every second
-            const bool two = 2 * (w.u % a.nrp) + 1 < a.nrt;
-            const int by = two ? 1 : 2, steps = two ? w.n : (w.n + 1 - g) / 2;
-            const int releases = two ? 1 : users;  // the group alone releases a block of one tile
-            const uint64_t qd = qd0 + (uint64_t)((two ? g : 0) * (QK_BYTES / 16));  // descriptors count 16 bytes
-            Ring k = k0, v = v0;
-            if (!two && g == 1) k.next(1, a.nk), v.next(1, a.nv);
-            ok = wait(smem_addr(&bars->q_full), (uint32_t)piece & 1u);
-            fence_proxy_async_smem();  // a gathered query operand, written by the softmax warps
-            // halves of the group's blocks: P.V of one, then S of the same half of the next block,
-            // while the softmax works on the other half
-            for (int n = -2; ok && n < 2 * steps; ++n) {
-                const int h = n & 1;
-                if (n >= 0) {
-                    ok = (h || wait(smem_addr(&bars->v_full[v.slot]), v.phase)) && wait(p_full + h * 8, (pv >> 1) & 1u);
-                    if (!ok) break;
-                    tc_fence_after();
-                    const uint64_t vd = vd0 + (uint64_t)(v.slot * (V_BYTES / 16) + h * (HK * 8));
-#pragma unroll
-                    for (int kk = 0; kk < HK / 16; ++kk)
-                        umma_f16_tmem_a_elect(o_tm, s_tm + h * HK + kk * 8, vd + kk * 128, idesc_pv,
-                                              kk > 0 || n > 0 ? 1u : 0u);
-                    umma_commit_elect(pv_done);
-                    if (h) {
-                        for (int r = 0; r < releases; ++r) umma_commit_elect(smem_addr(&bars->v_empty[v.slot]));
-                        v.next(by, a.nv);
-                    }
-                    ++pv;
-                }
-                if (n + 2 < 2 * steps) {
-                    ok = h || wait(smem_addr(&bars->k_full[k.slot]), k.phase);
-                    // the P.V just issued reads P, which lies over this half's S
-                    if (ok && n >= 0) ok = wait(pv_done, (pv - 1) & 1u);
-                    if (!ok) break;
-                    if (!kAll) fence_proxy_async_smem();  // copied keys, read by the tensor cores
-                    tc_fence_after();
-                    const uint64_t kd = kd0 + (uint64_t)(k.slot * (QK_BYTES / 16) + h * (kp * 8));
-                    if (kAll) {
-#pragma unroll
-                        for (int kk = 0; kk < D / 16; ++kk)
-                            umma_f16_elect(s_tm + h * HK, qd + (kk >> 2) * (BM * 8) + (kk & 3) * 2, kd + kk * 128,
-                                           idesc_s, kk > 0 ? 1u : 0u);
-                    } else {
-                        uint64_t q1 = qd, k1 = kd;
-#pragma unroll 1
-                        for (int kk = 0; kk < k_steps; ++kk, q1 += 128, k1 += 128)
-                            umma_f16_elect(s_tm + h * HK, q1, k1, idesc_s, kk > 0 ? 1u : 0u);
-                    }
-                    umma_commit_elect(s_full + h * 8);
-                    if (h) {
-                        for (int r = 0; r < releases; ++r) umma_commit_elect(smem_addr(&bars->k_empty[k.slot]));
-                        k.next(by, a.nk);
-                    }
-                }
-            }
-            if (ok) umma_commit_elect(smem_addr(&bars->o_full));
-            for (int j = 0; j < w.n; ++j) k0.next(1, a.nk), v0.next(1, a.nv);
-        }
-        __syncwarp();
-        umma_commit_elect(smem_addr(&bars->drain));
-        // issued MMAs finish on their own; TMEM is not freed under them
-        volatile int no_abort = 0;
-        mbar_wait(smem_addr(&bars->drain), 0, status, &no_abort);
-        __syncwarp();
-    } else if (warp < kMmaWarp) {
+    // With the gather warps the block has 512 threads of 128 registers; a softmax thread holds 64
+    // logits and wants more.  256 x 184 + 256 x 64 = 63488 of the 65536.
+    if (warp < kMmaWarp) {
+        if (!kAll) asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
         // ------------------------------------------------------------ softmax, query operand, output
         const int grp = warp >> 2, i = tid & 127;  // group, row of the tile = TMEM lane
         const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
-        const uint32_t s_col = tmem + lane_base + grp * BK, meet = smem_addr(&bars->meet);
+        const uint32_t s_col = tmem + lane_base + grp * 128, meet = smem_addr(&bars->meet);
         float* xch = reinterpret_cast<float*>(sQ);  // maxima and sums of the two groups (sQ is free by then)
         int piece = 0, meets = 0, queries = 0;
         Ring v0;  // the piece's first block in the value ring
         const uint32_t s_full = smem_addr(&bars->s_full[grp][0]), p_full = smem_addr(&bars->p_full[grp][0]);
         const uint32_t pv_done = smem_addr(&bars->pv_done[grp]);
-        uint32_t halves = 0;  // of this group, over all pieces
+        uint32_t blocks = 0;  // of this group, over all pieces: a block's buffer is blocks & 1
         // all softmax warps meet (bounded)
         auto together = [&]() -> bool {
             __syncwarp();
@@ -513,7 +355,7 @@ __global__ void __launch_bounds__(kThreadsTree, 1)
                     mbar_arrive_expect_tx(qf, (two ? 2 : 1) * BM * 256);
                     for (int t = 0; t < (two ? 2 : 1); ++t)
                         for (int h = 0; h < 2; ++h)
-                            tma_load_2d(qb + t * QK_BYTES + h * BM * 128, &qmap, qf, h * 64,
+                            tma_load_2d(qb + t * Q_BYTES + h * BM * 128, &qmap, qf, h * 64,
                                         (int)(row0 + (2 * rp + t) * BM));
                 }
                 ++queries;
@@ -530,7 +372,7 @@ __global__ void __launch_bounds__(kThreadsTree, 1)
 #pragma unroll
                     for (int e = 0; e < 8; ++e)
                         v[e] = dim >= 0 && r + e < a.R ? a.Q[(row0 + r + e) * D + dim] : (uint16_t)0;
-                    st_shared_v4(smem_addr(sQ + t * QK_BYTES) + swz(jr, c16, kp * 128),
+                    st_shared_v4(smem_addr(sQ + t * Q_BYTES) + swz(jr, c16, kp * 128),
                                  make_uint4(v[0] | ((uint32_t)v[1] << 16), v[2] | ((uint32_t)v[3] << 16),
                                             v[4] | ((uint32_t)v[5] << 16), v[6] | ((uint32_t)v[7] << 16)));
                 }
@@ -546,19 +388,20 @@ __global__ void __launch_bounds__(kThreadsTree, 1)
             float m_use = -INFINITY, l = 0.0f;
             Ring v = v0;
             if (!two && grp == 1) v.next(1, a.nv);
-            for (int n = 0; n < 2 * mine; ++n, ++halves) {
-                const int h = n & 1, key0 = (w.blk + (two ? n >> 1 : (n & ~1) + grp)) * BK + h * HK;
-                if (!__all_sync(0xffffffffu, mbar_wait(s_full + h * 8, (halves >> 1) & 1u, status, abort_flag))) {
+            for (int n = 0; n < mine; ++n, ++blocks) {
+                const uint32_t buf = blocks & 1u;
+                const int key0 = (w.blk + (two ? n : 2 * n + grp)) * BK;
+                if (!__all_sync(0xffffffffu, mbar_wait(s_full + buf * 8, (blocks >> 1) & 1u, status, abort_flag))) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
                 if (busy) {
                     uint32_t x[2][32];
-                    tmem_ld_32x32b_x32(s_col + h * HK, x[0]);
-                    tmem_ld_32x32b_x32(s_col + h * HK + 32, x[1]);
+                    tmem_ld_32x32b_x32(s_col + buf * BK, x[0]);
+                    tmem_ld_32x32b_x32(s_col + buf * BK + 32, x[1]);
                     tmem_ld_wait();
-                    if (key0 + HK > len) hide(x, way, key0, len);  // the half reaches the tree's slots
+                    if (key0 + BK > len) hide(x, way, key0, len);  // the block reaches the tree's slots
                     float mx[4];
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
@@ -576,8 +419,8 @@ __global__ void __launch_bounds__(kThreadsTree, 1)
                         const float alpha = resc ? exp2f(m_use - m_new) : 1.0f;
                         m_use = m_new;
                         l *= alpha;
-                        if (n > 0) {  // O holds the halves before: they are added once the last P.V is done
-                            if (!__all_sync(0xffffffffu, mbar_wait(pv_done, (halves - 1) & 1u, status, abort_flag))) {
+                        if (n > 0) {  // O holds the blocks before once the last P.V is done
+                            if (!__all_sync(0xffffffffu, mbar_wait(pv_done, (blocks - 1) & 1u, status, abort_flag))) {
                                 ok = false;
                                 break;
                             }
@@ -594,11 +437,11 @@ __global__ void __launch_bounds__(kThreadsTree, 1)
                             }
                         }
                     }
-                    // P lies over this half's S, whose every column has been read
-                    l += exp_half(x, a.scale_log2, m_use == -INFINITY ? 0.0f : -m_use, s_col + h * HK);
+                    // P lies over this block's S, whose every column has been read
+                    l += exp_block(x, a.scale_log2, m_use == -INFINITY ? 0.0f : -m_use, s_col + buf * BK);
                     tmem_st_wait();
                 }
-                if (key0 + HK > len) {
+                if (key0 + BK > len) {
                     // slots that no node holds may contain anything: their values become zeros, two
                     // threads per key (with two tiles both groups write the same zeros)
                     const int slot = key0 + (i & 63) - len;
@@ -608,7 +451,7 @@ __global__ void __launch_bounds__(kThreadsTree, 1)
                         break;
                     }
                     if (slot >= a.T || (slot >= 0 && a.parents && tree_way(par, slot) == 0)) {
-                        const uint32_t vrow = smem_addr(sV + v.slot * V_BYTES) + (i >> 6) * V_CHUNK + (h * HK + (i & 63)) * 128;
+                        const uint32_t vrow = smem_addr(sV + v.slot * V_BYTES) + (i >> 6) * V_CHUNK + (i & 63) * 128;
 #pragma unroll
                         for (int e = 0; e < 8; ++e) st_shared_v4(vrow + ((e + lane) & 7) * 16, make_uint4(0, 0, 0, 0));
                     }
@@ -616,8 +459,8 @@ __global__ void __launch_bounds__(kThreadsTree, 1)
                 }
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(p_full + h * 8);
-                if (h) v.next(two ? 1 : 2, a.nv);
+                if (lane == 0) mbar_arrive(p_full + buf * 8);
+                v.next(two ? 1 : 2, a.nv);
             }
             if (!ok) break;
             for (int j = 0; j < w.n; ++j) v0.next(1, a.nv);
@@ -717,6 +560,163 @@ __global__ void __launch_bounds__(kThreadsTree, 1)
             mbar_wait(smem_addr(&bars->q_full), (uint32_t)(queries - 1) & 1u, status, &no_abort);
         }
         __syncwarp();
+    } else if (warp < kGatherWarp) {
+        if (!kAll) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+        if (warp == kTmaWarp) {
+            // ------------------------------------------------------------ value blocks (and key blocks, every dim kept)
+            if (lane == 0) {
+                int c = 0, c_keys = 0;  // blocks issued, and key blocks (one more after an abort)
+                Ring k, v;
+                bool ok = true;
+                for (bool more = w.next(a, bars, true); ok && more; more = w.next(a, bars, false)) {
+                    const int plane = w.b * a.Hkv + w.u / a.nrp;
+                    for (int j = 0; j < w.n; ++j, ++c) {
+                        const int key0 = (w.blk + j) * BK;
+                        if (kAll) {
+                            ok = mbar_wait(smem_addr(&bars->k_empty[k.slot]), k.phase ^ 1u, status, abort_flag);
+                            if (!ok) break;
+                            const uint32_t kf = smem_addr(&bars->k_full[k.slot]);
+                            mbar_arrive_expect_tx(kf, K_BYTES);
+                            tma_load_3d(smem_addr(sK + k.slot * K_BYTES), &kmap, kf, key0, 0, plane);
+                            ++c_keys;
+                            k.next(1, a.nk);
+                        }
+                        ok = mbar_wait(smem_addr(&bars->v_empty[v.slot]), v.phase ^ 1u, status, abort_flag);
+                        if (!ok) break;
+                        const uint32_t vb = smem_addr(sV + v.slot * V_BYTES), vf = smem_addr(&bars->v_full[v.slot]);
+                        mbar_arrive_expect_tx(vf, V_BYTES);
+                        tma_load_3d(vb, &vmap, vf, 0, key0, plane);
+                        tma_load_3d(vb + V_CHUNK, &vmap, vf, 64, key0, plane);
+                        v.next(1, a.nv);
+                    }
+                }
+                // no copy may still be landing when the CTA leaves (after an abort; else all were consumed)
+                volatile int no_abort = 0;
+                for (int j = max(0, c_keys - a.nk); j < c_keys; ++j)
+                    mbar_wait(smem_addr(&bars->k_full[j % a.nk]), (uint32_t)(j / a.nk) & 1u, status, &no_abort);
+                for (int j = max(0, c - a.nv); j < c; ++j)
+                    mbar_wait(smem_addr(&bars->v_full[j % a.nv]), (uint32_t)(j / a.nv) & 1u, status, &no_abort);
+            }
+            __syncwarp();
+        } else if (warp < kTmaWarp) {
+            // ------------------------------------------------------------ MMA issuers: a warp per group
+            // The warp stays together and every instruction elects its thread, so that descriptors
+            // are computed once for the warp: issued from a branch of one thread, a product took
+            // about 110 cycles whatever its size.
+            const int g = warp - kMmaWarp;
+            const uint32_t idesc_s = idesc_bf16_f32(BM, BK, kAll ? 0 : 1, 1);
+            const uint32_t idesc_pv = idesc_bf16_f32(BM, D, 0, 1);
+            const uint64_t qd0 = smem_desc_sw128(smem_addr(sQ), kAll ? 16 : kp * 128, 1024);
+            const uint64_t kd0 = smem_desc_sw128(smem_addr(sK), K_BYTES, 1024);
+            const uint64_t vd0 = smem_desc_sw128(smem_addr(sV), V_CHUNK, 1024);
+            const uint32_t s_tm = tmem + g * 128, o_tm = tmem + TM_O + g * D;
+            const uint32_t s_full = smem_addr(&bars->s_full[g][0]), p_full = smem_addr(&bars->p_full[g][0]);
+            const uint32_t pv_done = smem_addr(&bars->pv_done[g]);
+            const int k_steps = kp / 16;
+            auto wait = [&](uint32_t bar, uint32_t phase) -> bool {
+                return __all_sync(0xffffffffu, mbar_wait(bar, phase, status, abort_flag));
+            };
+            Ring k0, v0;              // the piece's first block
+            uint32_t pv = 0;          // P.V products issued: block pv of the group is in buffer pv & 1
+            int piece = 0;
+            bool ok = true;
+            for (bool more = w.next(a, bars, true); ok && more; more = w.next(a, bars, false), ++piece) {
+                // with two row tiles every block is this group's, with one every second
+                const bool two = 2 * (w.u % a.nrp) + 1 < a.nrt;
+                const int by = two ? 1 : 2, steps = two ? w.n : (w.n + 1 - g) / 2;
+                const int releases = two ? 1 : users;  // the group alone releases a block of one tile
+                const uint64_t qd = qd0 + (uint64_t)((two ? g : 0) * (Q_BYTES / 16));  // descriptors count 16 bytes
+                Ring k = k0, v = v0;
+                if (!two && g == 1) k.next(1, a.nk), v.next(1, a.nv);
+                ok = wait(smem_addr(&bars->q_full), (uint32_t)piece & 1u);
+                fence_proxy_async_smem();  // a gathered query operand, written by the softmax warps
+                // P.V of a block, then S of the block after next in the same buffer, while the softmax
+                // works on the block between
+                for (int n = -2; ok && n < steps; ++n) {
+                    const uint32_t buf = (pv + (n < 0 ? n : 0)) & 1u;  // of blocks n and n + 2
+                    if (n >= 0) {
+                        ok = wait(smem_addr(&bars->v_full[v.slot]), v.phase) && wait(p_full + buf * 8, (pv >> 1) & 1u);
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint64_t vd = vd0 + (uint64_t)(v.slot * (V_BYTES / 16));
+#pragma unroll
+                        for (int kk = 0; kk < BK / 16; ++kk)
+                            umma_f16_tmem_a_elect(o_tm, s_tm + buf * BK + kk * 8, vd + kk * 128, idesc_pv,
+                                                  kk > 0 || n > 0 ? 1u : 0u);
+                        umma_commit_elect(pv_done);
+                        for (int r = 0; r < releases; ++r) umma_commit_elect(smem_addr(&bars->v_empty[v.slot]));
+                        v.next(by, a.nv);
+                        ++pv;
+                    }
+                    if (n + 2 < steps) {
+                        ok = wait(smem_addr(&bars->k_full[k.slot]), k.phase);
+                        // the P.V just issued reads P, which lies over this buffer's S
+                        if (ok && n >= 0) ok = wait(pv_done, (pv - 1) & 1u);
+                        if (!ok) break;
+                        if (!kAll) fence_proxy_async_smem();  // copied keys, read by the tensor cores
+                        tc_fence_after();
+                        const uint64_t kd = kd0 + (uint64_t)(k.slot * (K_BYTES / 16));
+                        if (kAll) {
+#pragma unroll
+                            for (int kk = 0; kk < D / 16; ++kk)
+                                umma_f16_elect(s_tm + buf * BK, qd + (kk >> 2) * (BM * 8) + (kk & 3) * 2, kd + kk * 128,
+                                               idesc_s, kk > 0 ? 1u : 0u);
+                        } else {
+                            uint64_t q1 = qd, k1 = kd;
+#pragma unroll 1
+                            for (int kk = 0; kk < k_steps; ++kk, q1 += 128, k1 += 128)
+                                umma_f16_elect(s_tm + buf * BK, q1, k1, idesc_s, kk > 0 ? 1u : 0u);
+                        }
+                        umma_commit_elect(s_full + buf * 8);
+                        for (int r = 0; r < releases; ++r) umma_commit_elect(smem_addr(&bars->k_empty[k.slot]));
+                        k.next(by, a.nk);
+                    }
+                }
+                if (ok) umma_commit_elect(smem_addr(&bars->o_full));
+                for (int j = 0; j < w.n; ++j) k0.next(1, a.nk), v0.next(1, a.nv);
+            }
+            __syncwarp();
+            umma_commit_elect(smem_addr(&bars->drain));
+            // issued MMAs finish on their own; TMEM is not freed under them
+            volatile int no_abort = 0;
+            mbar_wait(smem_addr(&bars->drain), 0, status, &no_abort);
+            __syncwarp();
+        }
+    } else if (!kAll) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+        // ------------------------------------------------------------ kept rows of K^T, 16 bytes a copy
+        // Quarter-warps take every sixteenth kept row, a lane 8 keys of it.  A warp's copy
+        // instruction takes about 110 cycles to leave, so that two warps of them bounded the
+        // kernel (1750 cycles a block at 64 kept dims, where its bytes take 1000).
+        const int c16 = lane & 7, row = (warp - kGatherWarp) * 4 + (lane >> 3);
+        Ring k;
+        bool ok = true;
+        for (bool more = w.next(a, bars, true); ok && more; more = w.next(a, bars, false)) {
+            const int plane = w.b * a.Hkv + w.u / a.nrp;
+            uint32_t at[8];  // the rows' places in the d-major cache; the padding repeats a kept row
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (16 * i < kp) at[i] = (uint32_t)a.idx[(size_t)plane * a.k + (16 * i + row < a.k ? 16 * i + row : 0)] * a.ldL;
+            const uint16_t* Kg = a.Kt + (size_t)plane * D * a.ldL + c16 * 8;
+            for (int j = 0; j < w.n; ++j) {
+                const int key0 = (w.blk + j) * BK;
+                if (!__all_sync(0xffffffffu,
+                                mbar_wait(smem_addr(&bars->k_empty[k.slot]), k.phase ^ 1u, status, abort_flag))) {
+                    ok = false;
+                    break;
+                }
+                // row 16 i + row lies at 2048 i + 128 row, its 16-byte pieces permuted by row mod 8
+                const uint32_t dst = smem_addr(sK + k.slot * K_BYTES) + row * 128 + ((c16 ^ (row & 7)) << 4);
+                const uint32_t bytes = key0 + c16 * 8 < a.ldL ? 16u : 0u;
+                const uint16_t* src = bytes ? Kg + key0 : Kg;
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (16 * i < kp) cp_async_16(dst + 2048 * i, src + at[i], bytes);
+                cp_async_arrive_noinc(smem_addr(&bars->k_full[k.slot]));
+                k.next(1, a.nk);
+            }
+        }
+        cp_async_wait_all();  // no copy may still be landing when the CTA leaves
     }
 
     tc_fence_before();
@@ -725,52 +725,79 @@ __global__ void __launch_bounds__(kThreadsTree, 1)
     if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
 }
 
-// The partials of a unit that was cut, joined: thread (row, four dims).  Also the
-// zeros of empty slots.  Memory bound on what the cuts left in L2.
-__global__ void __launch_bounds__(256) attn_tree_join_kernel(const TreeArgs a, int ctas) {
-    const int U = a.Hkv * a.nrp;
+// The partials of a unit that was cut, joined; also the zeros of empty slots.  A CTA
+// takes 8 rows: a warp per row weighs the pieces, then two thread groups of
+// (row, four dims) add every second piece, eight loads in flight, and are added in
+// order.  Bound by the latency of three dependent reads from L2 (and, with many
+// rows, by the partials' bytes).
+constexpr int kJoinRows = 8, kJoinThreads = 2 * kJoinRows * 32;
+constexpr int kMaxCtas = 256;
+
+__global__ void __launch_bounds__(kJoinThreads) attn_tree_join_kernel(const TreeArgs a, int ctas) {
+    __shared__ float weight[kMaxCtas][kJoinRows];
+    __shared__ float inv_s[kJoinRows];
+    __shared__ float4 half[kJoinRows * 32];
+    const int U = a.Hkv * a.nrp, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int unit = blockIdx.x, b = unit / U, u = unit % U, g = u / a.nrp, rp = u % a.nrp;
+    const int r0 = blockIdx.y * kJoinRows, rows = min(2 * BM, a.R - rp * 2 * BM) - r0;
+    if (rows <= 0) return;
     pdl_wait();
     pdl_launch_dependents();
-    const int unit = blockIdx.x, b = unit / U, u = unit % U, g = u / a.nrp, rp = u % a.nrp;
-    const int rows = min(2 * BM, a.R - rp * 2 * BM);
     const long long lo = a.cum[b], nb = (a.cum[b + 1] - lo) / U, total = a.cum[a.B];
     const long long C = min((long long)ctas, total);
-    const size_t row0 = ((size_t)b * a.Hkv + g) * a.R + rp * 2 * BM;
     const long long p0 = lo + u * nb, p1 = p0 + nb;  // the unit's blocks
     // share c is [total c / C, total (c + 1) / C): the shares of its first and last block
     const int c0 = nb ? (int)(((p0 + 1) * C - 1) / total) : 0, c1 = nb ? (int)((p1 * C - 1) / total) : 0;
     if (nb && c0 == c1) return;
-    for (int it = blockIdx.y * 256 + threadIdx.x; it < rows * 32; it += gridDim.y * 256) {
-        const int r = it % rows, c4 = it / rows;
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (nb) {
-            const size_t sf = slot_floats(a.slot_rows);
-            // the first share may have begun with another unit: its piece is then its second
-            const float* first = a.partials + (size_t)(2 * c0 + (total * c0 / C < p0 ? 1 : 0)) * sf;
-            float M = -INFINITY;
-            for (int c = c0; c <= c1; ++c)
-                M = fmaxf(M, (c == c0 ? first : a.partials + (size_t)2 * c * sf)[D * a.slot_rows + r]);
-            float L = 0.f;
-            if (M > -INFINITY) {
-#pragma unroll 4
-                for (int c = c0; c <= c1; ++c) {
-                    const float* s = c == c0 ? first : a.partials + (size_t)2 * c * sf;
-                    const float w = exp2f(s[D * a.slot_rows + r] - M);
-                    const float4 v = *reinterpret_cast<const float4*>(s + ((size_t)c4 * a.slot_rows + r) * 4);
-                    if (w > 0.f) {
-                        L = fmaf(w, s[(D + 1) * a.slot_rows + r], L);
-                        o.x = fmaf(w, v.x, o.x);
-                        o.y = fmaf(w, v.y, o.y);
-                        o.z = fmaf(w, v.z, o.z);
-                        o.w = fmaf(w, v.w, o.w);
-                    }
-                }
-            }
-            const float inv = L > 0.f ? 1.0f / L : 0.f;
-            o = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+    const int n = nb ? c1 - c0 + 1 : 0;
+    const size_t sf = slot_floats(a.slot_rows);
+    // the first share may have begun with another unit: its piece is then its second
+    const int skip = nb && total * c0 / C < p0 ? 1 : 0;
+    const float* base = a.partials + (size_t)(2 * c0) * sf;
+    auto piece = [&](int i) -> const float* { return base + (size_t)(2 * i + (i == 0 ? skip : 0)) * sf; };
+    if (warp < kJoinRows && warp < rows) {
+        const int r = r0 + warp;
+        float M = -INFINITY, L = 0.f;
+        for (int i = lane; i < n; i += 32) {
+            const float m = piece(i)[D * a.slot_rows + r];
+            weight[i][warp] = m;
+            M = fmaxf(M, m);
         }
-        *reinterpret_cast<uint2*>(a.O + (row0 + r) * D + c4 * 4) =
-            make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+        for (int i = lane; i < n; i += 32) {
+            const float wt = M == -INFINITY ? 0.f : exp2f(weight[i][warp] - M);
+            weight[i][warp] = wt;
+            L = fmaf(wt, piece(i)[(D + 1) * a.slot_rows + r], L);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+        if (lane == 0) inv_s[warp] = L > 0.f ? 1.0f / L : 0.f;
+    }
+    __syncthreads();
+    const int r = tid & (kJoinRows - 1), c4 = (tid / kJoinRows) & 31, grp = tid / (kJoinRows * 32);
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (r < rows) {
+        const size_t at = ((size_t)c4 * a.slot_rows + r0 + r) * 4;
+#pragma unroll 8
+        for (int i = grp; i < n; i += 2) {
+            const float wt = weight[i][r];
+            const float4 v = *reinterpret_cast<const float4*>(piece(i) + at);
+            if (wt > 0.f) {  // a piece in which the row saw nothing may hold anything
+                o.x = fmaf(wt, v.x, o.x);
+                o.y = fmaf(wt, v.y, o.y);
+                o.z = fmaf(wt, v.z, o.z);
+                o.w = fmaf(wt, v.w, o.w);
+            }
+        }
+    }
+    if (grp == 1) half[tid - kJoinRows * 32] = o;
+    __syncthreads();
+    if (grp == 0 && r < rows) {
+        const float4 h = half[tid];
+        const float inv = inv_s[r];
+        *reinterpret_cast<uint2*>(a.O + (((size_t)b * a.Hkv + g) * a.R + rp * 2 * BM + r0 + r) * D + c4 * 4) =
+            make_uint2(pack2((o.x + h.x) * inv, (o.y + h.y) * inv), pack2((o.z + h.z) * inv, (o.w + h.w) * inv));
     }
 }
 
@@ -800,14 +827,19 @@ __global__ void __launch_bounds__(256) tree_dims_kernel(const TreeArgs a) {
     const int c16 = tid & 15, rl = tid >> 4;
     uint32_t m[4] = {0, 0, 0, 0};  // two dims each, magnitudes of 15 bits
     const uint16_t* q = a.Q + (size_t)plane * a.R * D + c16 * 8;
-#pragma unroll 4
-    for (int r = rl; r < a.R; r += 16) {
-        if (!((there >> (r % a.T)) & 1)) continue;
-        const uint4 v = ld_nc_v4(q + (size_t)r * D);
-        m[0] = __vmaxu2(m[0], v.x & 0x7FFF7FFFu);
-        m[1] = __vmaxu2(m[1], v.y & 0x7FFF7FFFu);
-        m[2] = __vmaxu2(m[2], v.z & 0x7FFF7FFFu);
-        m[3] = __vmaxu2(m[3], v.w & 0x7FFF7FFFu);
+    for (int r0 = rl; r0 < a.R; r0 += 128) {  // eight rows in flight
+        uint4 v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            v[i] = r0 + 16 * i < a.R ? ld_nc_v4(q + (size_t)(r0 + 16 * i) * D) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t keep = (there >> ((r0 + 16 * i) % a.T)) & 1 ? 0x7FFF7FFFu : 0u;  // absent nodes do not count
+            m[0] = __vmaxu2(m[0], v[i].x & keep);
+            m[1] = __vmaxu2(m[1], v[i].y & keep);
+            m[2] = __vmaxu2(m[2], v[i].z & keep);
+            m[3] = __vmaxu2(m[3], v[i].w & keep);
+        }
     }
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
@@ -850,6 +882,7 @@ TreePlan tree_plan(int B, int Hq, int Hkv, int T, int ldL, int num_sms) {
     p.nrp = (p.nrt + 1) / 2;
     p.slot_rows = p.R < 2 * BM ? (p.R + 3) / 4 * 4 : 2 * BM;
     const long long most = (long long)B * Hkv * p.nrp * ((ldL + BK - 1) / BK);
+    if (num_sms > 256) num_sms = 256;  // pieces of a unit the joining kernel weighs
     p.ctas = most < num_sms ? (int)most : num_sms;
     return p;
 }
@@ -885,15 +918,15 @@ cudaError_t launch_attn_tree(const CUtensorMap& qmap, const CUtensorMap& kmap, c
     a.kp = (k + 15) / 16 * 16;
     a.scale_log2 = scale * 1.4426950408889634f;
     // rings: two stages each, then more values and keys by turns while they fit
-    const int qk = a.kp * 256;
-    const int fixed = 1024 + (p.nrt > 1 ? 2 : 1) * qk + (int)sizeof(TreeBars) + kTreeMax * 4;
+    const int kb = a.kp * 128;
+    const int fixed = 1024 + (p.nrt > 1 ? 2 : 1) * a.kp * 256 + (int)sizeof(TreeBars) + kTreeMax * 4;
     a.nk = a.nv = 2;
     for (bool grew = true; grew;) {
         grew = false;
-        if (a.nv < kMaxStages && fixed + (a.nv + 1) * V_BYTES + a.nk * qk <= kSmemMax) ++a.nv, grew = true;
-        if (a.nk < kMaxStages && a.nk < a.nv && fixed + a.nv * V_BYTES + (a.nk + 1) * qk <= kSmemMax) ++a.nk, grew = true;
+        if (a.nv < kMaxStages && fixed + (a.nv + 1) * V_BYTES + a.nk * kb <= kSmemMax) ++a.nv, grew = true;
+        if (a.nk < kMaxStages && a.nk < a.nv && fixed + a.nv * V_BYTES + (a.nk + 1) * kb <= kSmemMax) ++a.nk, grew = true;
     }
-    const size_t smem = fixed + (size_t)a.nv * V_BYTES + (size_t)a.nk * qk;
+    const size_t smem = fixed + (size_t)a.nv * V_BYTES + (size_t)a.nk * kb;
     auto* kern = a.identity ? attn_tree_kernel<true> : attn_tree_kernel<false>;
     cudaError_t e = ensure_smem_limit(kern, smem);
     if (e != cudaSuccess) return e;
@@ -901,11 +934,11 @@ cudaError_t launch_attn_tree(const CUtensorMap& qmap, const CUtensorMap& kmap, c
         e = launch_pdl(tree_dims_kernel, dim3(B * Hkv), dim3(256), 0, stream, a);
         if (e != cudaSuccess) return e;
     }
-    e = launch_pdl(kern, dim3(p.ctas), dim3(kThreadsTree), smem, stream, qmap, kmap, vmap, a);
+    e = launch_pdl(kern, dim3(p.ctas), dim3(tree_threads(a.identity)), smem, stream, qmap, kmap, vmap, a);
     if (e != cudaSuccess) return e;
     const int most_rows = p.R < 2 * BM ? p.R : 2 * BM;
-    return launch_pdl(attn_tree_join_kernel, dim3(B * Hkv * p.nrp, (most_rows * 32 + 255) / 256), dim3(256), 0, stream, a,
-                      p.ctas);
+    return launch_pdl(attn_tree_join_kernel, dim3(B * Hkv * p.nrp, (most_rows + kJoinRows - 1) / kJoinRows),
+                      dim3(kJoinThreads), 0, stream, a, p.ctas);
 }
 
 }  // namespace rmm
