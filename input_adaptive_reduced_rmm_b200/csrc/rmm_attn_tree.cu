@@ -335,25 +335,17 @@ __global__ void __launch_bounds__(tree_threads(kAll), 1)
             if (lane == 0) mbar_arrive(meet);
             return __all_sync(0xffffffffu, mbar_wait(meet, (uint32_t)(meets++) & 1u, status, abort_flag));
         };
-        bool ok = true;
-        for (bool more = w.next(a, bars, true); ok && more; more = w.next(a, bars, false), ++piece) {
-            const int g = w.u / a.nrp, rp = w.u % a.nrp;
-            const bool two = 2 * rp + 1 < a.nrt;
-            const int plane = w.b * a.Hkv + g;
-            const int len = a.lens[w.b];
-            const int tile = 2 * rp + (two ? grp : 0);
-            const int row = tile * BM + i;  // of the unit's G * T rows: query head row / T, node row % T
+        // the tree and the query operand of the piece at `w`
+        auto open = [&]() {
+            const int rp = w.u % a.nrp, plane = w.b * a.Hkv + w.u / a.nrp;
+            const int tiles = 2 * rp + 1 < a.nrt ? 2 : 1;
             const size_t row0 = (size_t)plane * a.R;
-            // the tree and the query operand; the piece before is done with both (and with the
-            // maxima and sums that lay where a copy now writes)
-            fence_proxy_async_smem();
-            if (!together()) break;
             if (a.parents && tid < a.T) par[tid] = a.parents[(size_t)w.b * a.T + tid];
             if (kAll) {
                 if (tid == 0) {
                     const uint32_t qf = smem_addr(&bars->q_full), qb = smem_addr(sQ);
-                    mbar_arrive_expect_tx(qf, (two ? 2 : 1) * BM * 256);
-                    for (int t = 0; t < (two ? 2 : 1); ++t)
+                    mbar_arrive_expect_tx(qf, tiles * BM * 256);
+                    for (int t = 0; t < tiles; ++t)
                         for (int h = 0; h < 2; ++h)
                             tma_load_2d(qb + t * Q_BYTES + h * BM * 128, &qmap, qf, h * 64,
                                         (int)(row0 + (2 * rp + t) * BM));
@@ -361,9 +353,8 @@ __global__ void __launch_bounds__(tree_threads(kAll), 1)
                 ++queries;
                 if (w.blk == 0 && rp == 0 && a.idx && tid < D) a.idx[(size_t)plane * D + tid] = tid;
             } else {
-                // the kept dims of 8 rows at a time; both groups share the work of one tile
+                // the kept dims of 8 rows at a time
                 const int32_t* S = a.idx + (size_t)plane * a.k;
-                const int tiles = two ? 2 : 1;
                 for (int it = tid; it < kp * 16 * tiles; it += kSoftmaxThreads) {
                     const int jr = it % kp, c16 = (it / kp) & 15, t = it / (kp * 16);
                     const int dim = jr < a.k ? S[jr] : -1;
@@ -379,7 +370,19 @@ __global__ void __launch_bounds__(tree_threads(kAll), 1)
                 fence_proxy_async_smem();
                 mbar_arrive(smem_addr(&bars->q_full));
             }
-            if (!together()) break;  // par
+        };
+        bool ok = true;
+        bool more = w.next(a, bars, true);
+        if (more) open();
+        for (; ok && more; ++piece) {
+            const int g = w.u / a.nrp, rp = w.u % a.nrp;
+            const bool two = 2 * rp + 1 < a.nrt;
+            const int plane = w.b * a.Hkv + g;
+            const int len = a.lens[w.b];
+            const int tile = 2 * rp + (two ? grp : 0);
+            const int row = tile * BM + i;  // of the unit's G * T rows: query head row / T, node row % T
+            const size_t row0 = (size_t)plane * a.R;
+            if (!together()) break;  // par; and the outputs of the piece before have been read
             uint64_t way = 0;
             if (row < a.R) way = a.parents ? tree_way(par, row % a.T) : chain_way(row % a.T);
             const bool busy = __any_sync(0xffffffffu, row < a.R);  // the warp has rows
@@ -473,6 +476,22 @@ __global__ void __launch_bounds__(tree_threads(kAll), 1)
             if (way == 0) m_use = -INFINITY, l = 0.0f;  // an absent node sees nothing
             const bool whole = w.n == w.nb;
             float* slot = a.partials + (size_t)(2 * blockIdx.x + (w.left == bars->blocks ? 0 : 1)) * slot_floats(a.slot_rows);
+            const bool second = w.n > 1;  // with one tile: group 1 had a block, O1 holds this unit's data
+            float m0 = 0.f, m1 = 0.f, l0 = 0.f, l1 = 0.f;
+            if (!two) {  // both groups hold a part of the same rows
+                xch[grp * BM + i] = m_use;
+                xch[2 * BM + grp * BM + i] = l;
+                if (!together()) break;
+                m0 = xch[i], m1 = xch[BM + i], l0 = xch[2 * BM + i], l1 = xch[3 * BM + i];
+            }
+            // the query operand (every S is done), the tree and the exchange are free: the next
+            // piece's products start under this one's output
+            fence_proxy_async_smem();
+            tc_fence_before();
+            if (!together()) break;
+            tc_fence_after();
+            more = w.next(a, bars, false);
+            if (more) open();
             if (two) {
                 const float inv = l > 0.0f ? 1.0f / l : 0.0f;
                 const int sr = grp * BM + i;
@@ -505,18 +524,11 @@ __global__ void __launch_bounds__(tree_threads(kAll), 1)
                     }
                 }
             } else {
-                // both groups hold a part of the same rows: join them, 64 dims each
-                xch[grp * BM + i] = m_use;
-                xch[2 * BM + grp * BM + i] = l;
-                tc_fence_before();
-                if (!together()) break;
-                tc_fence_after();
-                const float m0 = xch[i], m1 = xch[BM + i], l0 = xch[2 * BM + i], l1 = xch[3 * BM + i];
+                // join the groups' parts, 64 dims each
                 const float M = fmaxf(m0, m1);
                 const float w0 = m0 == -INFINITY ? 0.0f : exp2f(m0 - M), w1 = m1 == -INFINITY ? 0.0f : exp2f(m1 - M);
                 const float L = w0 * l0 + w1 * l1;
                 const float inv = whole ? (L > 0.0f ? 1.0f / L : 0.0f) : 1.0f;
-                const bool second = w.n > 1;  // group 1 had a step: O1 holds this unit's data
                 if (!whole && row < a.R && grp == 0) {
                     slot[D * a.slot_rows + i] = M;
                     slot[(D + 1) * a.slot_rows + i] = L;
@@ -725,26 +737,21 @@ __global__ void __launch_bounds__(tree_threads(kAll), 1)
     if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
 }
 
-// The partials of a unit that was cut, joined; also the zeros of empty slots.  A CTA
-// takes 8 rows: a warp per row weighs the pieces, then two thread groups of
-// (row, four dims) add every second piece, eight loads in flight, and are added in
-// order.  Bound by the latency of three dependent reads from L2 (and, with many
-// rows, by the partials' bytes).
-constexpr int kJoinRows = 8, kJoinThreads = 2 * kJoinRows * 32;
-constexpr int kMaxCtas = 256;
+// The partials of a unit that was cut, joined; also the zeros of empty slots.  A
+// thread takes four dims of a row, eight pieces in flight, with a running maximum.
+// Bound by the latency of two dependent reads from L2 and, with many rows, by the
+// partials' bytes.
+constexpr int kJoinRows = 8;
 
-__global__ void __launch_bounds__(kJoinThreads) attn_tree_join_kernel(const TreeArgs a, int ctas) {
-    __shared__ float weight[kMaxCtas][kJoinRows];
-    __shared__ float inv_s[kJoinRows];
-    __shared__ float4 half[kJoinRows * 32];
-    const int U = a.Hkv * a.nrp, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+__global__ void __launch_bounds__(kJoinRows * 32) attn_tree_join_kernel(const TreeArgs a, int ctas) {
+    const int U = a.Hkv * a.nrp, tid = threadIdx.x;
     const int unit = blockIdx.x, b = unit / U, u = unit % U, g = u / a.nrp, rp = u % a.nrp;
-    const int r0 = blockIdx.y * kJoinRows, rows = min(2 * BM, a.R - rp * 2 * BM) - r0;
-    if (rows <= 0) return;
+    const int r = blockIdx.y * kJoinRows + (tid & (kJoinRows - 1)), c4 = tid / kJoinRows;
+    if (r >= min(2 * BM, a.R - rp * 2 * BM)) return;
     pdl_wait();
     pdl_launch_dependents();
-    const long long lo = a.cum[b], nb = (a.cum[b + 1] - lo) / U, total = a.cum[a.B];
-    const long long C = min((long long)ctas, total);
+    const long long lo = a.cum[b], hi = a.cum[b + 1], total = a.cum[a.B];
+    const long long nb = (hi - lo) / U, C = min((long long)ctas, total);
     const long long p0 = lo + u * nb, p1 = p0 + nb;  // the unit's blocks
     // share c is [total c / C, total (c + 1) / C): the shares of its first and last block
     const int c0 = nb ? (int)(((p0 + 1) * C - 1) / total) : 0, c1 = nb ? (int)((p1 * C - 1) / total) : 0;
@@ -754,51 +761,43 @@ __global__ void __launch_bounds__(kJoinThreads) attn_tree_join_kernel(const Tree
     // the first share may have begun with another unit: its piece is then its second
     const int skip = nb && total * c0 / C < p0 ? 1 : 0;
     const float* base = a.partials + (size_t)(2 * c0) * sf;
-    auto piece = [&](int i) -> const float* { return base + (size_t)(2 * i + (i == 0 ? skip : 0)) * sf; };
-    if (warp < kJoinRows && warp < rows) {
-        const int r = r0 + warp;
-        float M = -INFINITY, L = 0.f;
-        for (int i = lane; i < n; i += 32) {
-            const float m = piece(i)[D * a.slot_rows + r];
-            weight[i][warp] = m;
-            M = fmaxf(M, m);
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-        for (int i = lane; i < n; i += 32) {
-            const float wt = M == -INFINITY ? 0.f : exp2f(weight[i][warp] - M);
-            weight[i][warp] = wt;
-            L = fmaf(wt, piece(i)[(D + 1) * a.slot_rows + r], L);
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
-        if (lane == 0) inv_s[warp] = L > 0.f ? 1.0f / L : 0.f;
-    }
-    __syncthreads();
-    const int r = tid & (kJoinRows - 1), c4 = (tid / kJoinRows) & 31, grp = tid / (kJoinRows * 32);
+    const size_t at = ((size_t)c4 * a.slot_rows + r) * 4;
+    float M = -INFINITY, L = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (r < rows) {
-        const size_t at = ((size_t)c4 * a.slot_rows + r0 + r) * 4;
-#pragma unroll 8
-        for (int i = grp; i < n; i += 2) {
-            const float wt = weight[i][r];
-            const float4 v = *reinterpret_cast<const float4*>(piece(i) + at);
-            if (wt > 0.f) {  // a piece in which the row saw nothing may hold anything
-                o.x = fmaf(wt, v.x, o.x);
-                o.y = fmaf(wt, v.y, o.y);
-                o.z = fmaf(wt, v.z, o.z);
-                o.w = fmaf(wt, v.w, o.w);
+    constexpr int kFly = 8;
+    for (int i0 = 0; i0 < n; i0 += kFly) {
+        float m[kFly], l[kFly];
+        float4 v[kFly];
+#pragma unroll
+        for (int i = 0; i < kFly; ++i) {
+            const float* p = base + (size_t)(2 * min(i0 + i, n - 1) + (i0 + i == 0 ? skip : 0)) * sf;
+            m[i] = i0 + i < n ? p[D * a.slot_rows + r] : -INFINITY;
+            l[i] = p[(D + 1) * a.slot_rows + r];
+            v[i] = *reinterpret_cast<const float4*>(p + at);
+        }
+        float top = M;
+#pragma unroll
+        for (int i = 0; i < kFly; ++i) top = fmaxf(top, m[i]);
+        if (top == -INFINITY) continue;  // the row has seen no key
+        const float keep = exp2f(M - top);
+        M = top;
+        L *= keep;
+        o.x *= keep, o.y *= keep, o.z *= keep, o.w *= keep;
+#pragma unroll
+        for (int i = 0; i < kFly; ++i) {
+            const float w = exp2f(m[i] - M);
+            if (w > 0.f) {  // a piece in which the row saw nothing may hold anything
+                L = fmaf(w, l[i], L);
+                o.x = fmaf(w, v[i].x, o.x);
+                o.y = fmaf(w, v[i].y, o.y);
+                o.z = fmaf(w, v[i].z, o.z);
+                o.w = fmaf(w, v[i].w, o.w);
             }
         }
     }
-    if (grp == 1) half[tid - kJoinRows * 32] = o;
-    __syncthreads();
-    if (grp == 0 && r < rows) {
-        const float4 h = half[tid];
-        const float inv = inv_s[r];
-        *reinterpret_cast<uint2*>(a.O + (((size_t)b * a.Hkv + g) * a.R + rp * 2 * BM + r0 + r) * D + c4 * 4) =
-            make_uint2(pack2((o.x + h.x) * inv, (o.y + h.y) * inv), pack2((o.z + h.z) * inv, (o.w + h.w) * inv));
-    }
+    const float inv = L > 0.f ? 1.0f / L : 0.f;
+    *reinterpret_cast<uint2*>(a.O + (((size_t)b * a.Hkv + g) * a.R + rp * 2 * BM + r) * D + c4 * 4) =
+        make_uint2(pack2(o.x * inv, o.y * inv), pack2(o.z * inv, o.w * inv));
 }
 
 // The kept dims of one (sequence, KV head): the column maximum of |Q| over the
@@ -882,7 +881,6 @@ TreePlan tree_plan(int B, int Hq, int Hkv, int T, int ldL, int num_sms) {
     p.nrp = (p.nrt + 1) / 2;
     p.slot_rows = p.R < 2 * BM ? (p.R + 3) / 4 * 4 : 2 * BM;
     const long long most = (long long)B * Hkv * p.nrp * ((ldL + BK - 1) / BK);
-    if (num_sms > 256) num_sms = 256;  // pieces of a unit the joining kernel weighs
     p.ctas = most < num_sms ? (int)most : num_sms;
     return p;
 }
@@ -938,7 +936,7 @@ cudaError_t launch_attn_tree(const CUtensorMap& qmap, const CUtensorMap& kmap, c
     if (e != cudaSuccess) return e;
     const int most_rows = p.R < 2 * BM ? p.R : 2 * BM;
     return launch_pdl(attn_tree_join_kernel, dim3(B * Hkv * p.nrp, (most_rows + kJoinRows - 1) / kJoinRows),
-                      dim3(kJoinThreads), 0, stream, a, p.ctas);
+                      dim3(kJoinRows * 32), 0, stream, a, p.ctas);
 }
 
 }  // namespace rmm
