@@ -159,13 +159,6 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     return r;
 }
 
-// two fp32 as packed bf16, `lo` in the low half
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-    uint32_t r;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-
 // p = 2^(x scale - m) for 64 logits of a row, their sum, and P (bf16) to the 32
 // columns at pcol.
 __device__ __forceinline__ float exp_block(const uint32_t (&x)[2][32], float scale_log2, float neg_m, uint32_t pcol) {

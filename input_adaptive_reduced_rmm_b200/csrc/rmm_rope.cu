@@ -5,16 +5,17 @@
 //   x'  = x / sqrt(mean_j x_j^2 + eps) * w                 (q and k, each head)
 //   (x'_i, x'_j) -> (x'_i c - x'_j s, x'_j c + x'_i s)     c + is = e^(i pos f_i)
 // for the rot/2 pairs (i, j) = (i, i + rot/2), or (2i, 2i+1) when interleaved.
-// Everything between the bf16 input and the one rounding to bf16 is fp32; the
-// angle pos * f_i is formed and reduced to a fraction of a turn in fp64 (an
-// fp32 angle is off by 0.004 rad at position 10^5), its sine and cosine in
-// fp32.
+// Everything between the bf16 input and the one rounding to bf16 is fp32.  The
+// angle is a fraction of a turn in 64-bit fixed point: pos * round(2^64 f / 2 pi)
+// modulo 2^64, off by less than 2^-33 of a turn at any position (an fp32 angle
+// is off by 0.004 rad at position 10^5), its sine and cosine are fp32.
 //
-// Memory bound: each element is read once and written once.  A half-warp holds
-// one (token, head) row of 128 dims, 8 per lane, so the norm and the partner of
-// a rotated pair are shuffles; it keeps a token's sines and cosines in registers
-// over the CTA's heads and has four heads' rows in flight.  With fewer than 16
-// tokens the half-warps share them and take different heads.  Keys go through a
+// Memory bound: each element is read once and written once.  A quarter-warp holds
+// one (token, head) row of 128 dims; a lane has 8 dims and the 8 that they are
+// rotated with, so only the norm's sum crosses lanes, and 8 angles serve both.  It
+// keeps a token's sines and cosines, times the norm's weights, in registers over
+// the CTA's heads and has two heads' rows in flight.  With fewer than 32 tokens
+// the quarter-warps share them and take different heads.  Keys go through a
 // shared tile to the d-major cache, written in 16-byte pieces of 8 slots where
 // all 8 belong to the call.
 #include "rmm_common.cuh"
@@ -30,7 +31,7 @@ constexpr int kRopeThreads = 256;
 constexpr int kRopeTokens = 32;   // tokens per CTA
 constexpr int kRopeHeads = 16;    // heads per CTA (q and v): the angles of a token serve them all
 constexpr int kRopeKeyHeads = 4;  // heads per CTA (k): one shared tile each
-constexpr int kFly = 4;           // heads' rows in flight
+constexpr int kFly = 2;           // heads' rows in flight
 constexpr int kTilePitch = kRopeTokens + 1;  // u16 per dim row of a key tile
 
 struct RopeArgs {
@@ -42,30 +43,53 @@ struct RopeArgs {
     float eps;
 };
 
-__device__ __forceinline__ void unpack8(const uint4& w, float (&f)[8]) {
+// Two fp32 side by side, as the packed arithmetic takes them.
+struct F2 {
+    uint64_t v;
+    __device__ __forceinline__ F2() {}
+    __device__ __forceinline__ F2(float lo, float hi) { asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(lo), "f"(hi)); }
+    __device__ __forceinline__ void get(float& lo, float& hi) const {
+        asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+    }
+};
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+
+__device__ __forceinline__ void unpack8(const uint4& w, F2 (&f)[4]) {
     const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
+    for (int e = 0; e < 4; ++e) f[e] = F2(__uint_as_float(u[e] << 16), __uint_as_float(u[e] & 0xFFFF0000u));
+}
+
+__device__ __forceinline__ uint4 pack8(const F2 (&f)[4]) {
+    uint32_t u[4];
+#pragma unroll
     for (int e = 0; e < 4; ++e) {
-        f[2 * e] = __uint_as_float(u[e] << 16);
-        f[2 * e + 1] = __uint_as_float(u[e] & 0xFFFF0000u);
+        float lo, hi;
+        f[e].get(lo, hi);
+        u[e] = pack2(lo, hi);
     }
+    return make_uint4(u[0], u[1], u[2], u[3]);
 }
 
-__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
-    return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
-                      pack_bf16x2(f[6], f[7]));
+// cos and sin of pos * f, with `turns` = 2^64 f / 2 pi modulo 2^64
+__device__ __forceinline__ void turn(int pos, uint64_t turns, float& c, float& s) {
+    const int32_t half = (int32_t)(((uint64_t)(uint32_t)pos * turns) >> 32);  // in units of 2^-31 half turns
+    sincospif((float)half * 4.656612873077393e-10f, &s, &c);
 }
 
-// cos and sin of pos * f; the product of a 31-bit position and a 24-bit
-// frequency is exact in fp64
-__device__ __forceinline__ void turn(int pos, float f, float& c, float& s) {
-    const double t = (double)pos * (double)f * 0.15915494309189533577;  // turns
-    sincospif(2.0f * (float)(t - rint(t)), &s, &c);
-}
-
-__global__ void __launch_bounds__(kRopeThreads) qkv_rope_kernel(const RopeArgs a) {
+__global__ void __launch_bounds__(kRopeThreads, 3) qkv_rope_kernel(const RopeArgs a) {
     __shared__ int32_t par[kTreeMax];
     __shared__ int pos_s[kRopeTokens];
+    __shared__ uint64_t freq[D / 2];  // 2^64 f / 2 pi modulo 2^64
     __shared__ uint16_t tile[kRopeKeyHeads][D * kTilePitch];
     const int tid = threadIdx.x;
     const int b = blockIdx.x / a.tiles, t0 = (blockIdx.x % a.tiles) * kRopeTokens;
@@ -85,113 +109,153 @@ __global__ void __launch_bounds__(kRopeThreads) qkv_rope_kernel(const RopeArgs a
         if (tid < a.T) par[tid] = a.parents[(size_t)b * a.T + tid];
         __syncthreads();
     }
+    if (tid >= 64 && tid < 64 + a.rot / 2) {
+        double t = (double)a.inv_freq[tid - 64] * 0.15915494309189533577;  // turns per position
+        t -= floor(t);
+        freq[tid - 64] = __double2ull_rn(t * 18446744073709551616.0);
+    }
     if (tid < nt) {
         int p = t0 + tid;
         if (a.parents) p = __popcll(tree_way(par, p)) - 1;  // depth; -1 when absent
         pos_s[tid] = p < 0 ? -1 : start + p;
     }
-    __syncthreads();
+    const bool holes = __syncthreads_or(tid < nt && pos_s[tid] < 0);  // absent nodes: their slots stay
 
-    const int l = tid & 15, hw = tid >> 4;  // dims 8l .. 8l+7 of the half-warp's row
-    const unsigned mask = 0xFFFFu << (tid & 16);
-    // half-warps over tokens, the rest over heads
-    const int tpar = nt >= 16 ? 16 : nt > 8 ? 16 : nt > 4 ? 8 : nt > 2 ? 4 : nt;
-    const int hpar = 16 / tpar, ho = hw / tpar;
-    const int half = a.rot >> 4;            // lanes of one half of the rotated dims
+    const int l = tid & 7, qw = tid >> 3;
+    const unsigned mask = 0xFFu << (tid & 24);
+    // quarter-warps over tokens, the rest over heads
+    const int tpar = nt > 16 ? 32 : nt > 8 ? 16 : nt > 4 ? 8 : nt > 2 ? 4 : nt;
+    const int hpar = 32 / tpar, ho = qw / tpar;
     const bool turns = kind != 2 && a.inv_freq;
-    const bool turned = turns && 8 * l < a.rot;
-    const int partner = a.interleaved ? l : (l < half ? l + half : l < 2 * half ? l - half : l);
-    const bool hi = l >= half;
+    // the lane's dims A .. A+7 and B .. B+7: pairs (A + e, B + e), or neighbours when interleaved
+    const int half = a.rot / 2;
+    int A = 16 * l, B = 16 * l + 8;
+    bool turned = turns && A < a.rot;
+    if (turns && !a.interleaved) {
+        turned = 8 * l < half;
+        A = turned ? 8 * l : a.rot + 2 * (8 * l - half);
+        B = turned ? 8 * l + half : A + 8;
+    }
     const uint16_t* Y = kind == 0 ? a.Yq : kind == 1 ? a.Yk : a.Yv;
     const uint16_t* wn = kind == 0 ? a.qn : kind == 1 ? a.kn : nullptr;
-    float w[8];
-    if (wn) unpack8(ld_nc_v4(wn + 8 * l), w);
 
-    // lanes of a half-warp agree on everything but l, so shuffles stay inside it
-    for (int tl = hw % tpar; tl < nt; tl += tpar) {
+    // lanes of a quarter-warp agree on everything but l, so shuffles stay inside it
+    for (int tl = qw % tpar; tl < nt; tl += tpar) {
         const int pos = pos_s[tl];
         if (pos < 0) continue;
         const size_t row = (size_t)b * a.T + t0 + tl;
-        const uint16_t* src = Y + (row * H + h0) * D + 8 * l;
-        float c[8], s[8];
-        if (turns) {
-            if (a.interleaved) {
+        const uint16_t* src = Y + (row * H + h0) * D;
+        uint4 na[kFly], nb[kFly];  // the next heads' rows
+        auto fetch = [&](int hb) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    c[e] = 1.f, s[e] = 0.f;
-                    if (turned) turn(pos, __ldg(a.inv_freq + 4 * l + e), c[e], s[e]);
+            for (int i = 0; i < kFly; ++i)
+                if (hb + i * hpar < nh) {
+                    na[i] = ld_nc_v4(src + (size_t)(hb + i * hpar) * D + A);
+                    nb[i] = ld_nc_v4(src + (size_t)(hb + i * hpar) * D + B);
                 }
-            } else {
-                // the two lanes of a pair of chunks share 8 angles: each forms four
-                float mc[4], ms[4];
+        };
+        fetch(ho);
+        // x = (a, b): a' = a ca + b sa, b' = b cb + a sb, where the angle's parts hold the norm's
+        // weights too: for pairs across a and b the factors are c w_a, -s w_b, c w_b, s w_a
+        F2 ca[4], sa[4], cb[4], sb[4];
+        {
+            F2 one[4] = {F2(1.f, 1.f), F2(1.f, 1.f), F2(1.f, 1.f), F2(1.f, 1.f)};
+            F2 wa[4], wb[4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    mc[e] = 1.f, ms[e] = 0.f;
-                    if (turned) turn(pos, __ldg(a.inv_freq + 8 * (hi ? l - half : l) + (hi ? 4 : 0) + e), mc[e], ms[e]);
+            for (int e = 0; e < 4; ++e) wa[e] = wb[e] = one[e];
+            if (wn) {
+                unpack8(ld_nc_v4(wn + A), wa);
+                unpack8(ld_nc_v4(wn + B), wb);
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                float c0 = 1.f, s0 = 0.f, c1 = 1.f, s1 = 0.f;
+                if (turned) {
+                    turn(pos, freq[8 * l + 2 * e], c0, s0);
+                    turn(pos, freq[8 * l + 2 * e + 1], c1, s1);
                 }
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float oc = __shfl_sync(mask, mc[e], partner, 16);
-                    const float os = __shfl_sync(mask, ms[e], partner, 16);
-                    c[e] = hi ? oc : mc[e];
-                    s[e] = hi ? os : ms[e];
-                    c[4 + e] = hi ? mc[e] : oc;
-                    s[4 + e] = hi ? ms[e] : os;
+                if (a.interleaved) {
+                    // angles 2e, 2e+1 of the lane's 8 belong to the neighbours of word pair e: those of a
+                    // for e < 2, of b above; their (c, c) and (-s, s), weights of the partner in the second
+                    F2* cx = e < 2 ? ca : cb;
+                    F2* sx = e < 2 ? sa : sb;
+                    const F2* wx = e < 2 ? wa : wb;
+                    const int k = 2 * (e & 1);
+                    float u, v;
+                    wx[k].get(u, v);
+                    cx[k] = F2(u * c0, v * c0);
+                    sx[k] = F2(-v * s0, u * s0);
+                    wx[k + 1].get(u, v);
+                    cx[k + 1] = F2(u * c1, v * c1);
+                    sx[k + 1] = F2(-v * s1, u * s1);
+                } else {
+                    ca[e] = mul2(wa[e], F2(c0, c1));
+                    cb[e] = mul2(wb[e], F2(c0, c1));
+                    sa[e] = mul2(wb[e], F2(-s0, -s1));
+                    sb[e] = mul2(wa[e], F2(s0, s1));
                 }
             }
         }
         for (int hb = ho; hb < nh; hb += hpar * kFly) {
-            uint4 raw[kFly];
+            uint4 ra[kFly], rb[kFly];
 #pragma unroll
-            for (int i = 0; i < kFly; ++i)
-                if (hb + i * hpar < nh) raw[i] = ld_nc_v4(src + (size_t)(hb + i * hpar) * D);
+            for (int i = 0; i < kFly; ++i) ra[i] = na[i], rb[i] = nb[i];
+            fetch(hb + hpar * kFly);
 #pragma unroll
             for (int i = 0; i < kFly; ++i) {
                 const int h = hb + i * hpar;
                 if (h >= nh) break;
                 if (wn || turns) {
-                    float x[8];
-                    unpack8(raw[i], x);
+                    F2 x[4], y[4];
+                    unpack8(ra[i], x);
+                    unpack8(rb[i], y);
+                    float inv = 1.0f;
                     if (wn) {
-                        float ss = 0.f;
+                        F2 s2 = mul2(x[0], x[0]);
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
+                        for (int e = 1; e < 4; ++e) s2 = fma2(x[e], x[e], s2);
 #pragma unroll
-                        for (int o = 8; o > 0; o >>= 1) ss += __shfl_xor_sync(mask, ss, o, 16);
-                        const float inv = rsqrtf(ss * (1.0f / D) + a.eps);
+                        for (int e = 0; e < 4; ++e) s2 = fma2(y[e], y[e], s2);
+                        float s0, s1;
+                        s2.get(s0, s1);
+                        float ss = s0 + s1;
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) x[e] = x[e] * inv * w[e];
+                        for (int o = 4; o > 0; o >>= 1) ss += __shfl_xor_sync(mask, ss, o, 8);
+                        inv = rsqrtf(ss * (1.0f / D) + a.eps);
                     }
-                    if (turns) {
-                        if (a.interleaved) {
-                            if (turned) {
+                    const F2 i2(inv, inv);
+                    F2 p[4], q[4];
 #pragma unroll
-                                for (int e = 0; e < 4; ++e) {
-                                    const float u = x[2 * e], v = x[2 * e + 1];
-                                    x[2 * e] = u * c[e] - v * s[e];
-                                    x[2 * e + 1] = v * c[e] + u * s[e];
-                                }
-                            }
-                        } else {
-#pragma unroll
-                            for (int e = 0; e < 8; ++e) {
-                                const float y = __shfl_sync(mask, x[e], partner, 16);
-                                if (turned) x[e] = x[e] * c[e] + (hi ? y : -y) * s[e];
-                            }
+                    for (int e = 0; e < 4; ++e) {
+                        F2 xs = y[e], ys = x[e];
+                        if (a.interleaved) {  // a neighbour's partner is the other half of its word
+                            float u, v;
+                            x[e].get(u, v);
+                            xs = F2(v, u);
+                            y[e].get(u, v);
+                            ys = F2(v, u);
                         }
+                        p[e] = mul2(fma2(x[e], ca[e], mul2(xs, sa[e])), i2);
+                        q[e] = mul2(fma2(y[e], cb[e], mul2(ys, sb[e])), i2);
                     }
-                    raw[i] = pack8(x);
+                    ra[i] = pack8(p);
+                    rb[i] = pack8(q);
                 }
-                if (kind == 0) {
-                    *reinterpret_cast<uint4*>(a.Q + (((size_t)b * a.Hq + h0 + h) * a.T + t0 + tl) * D + 8 * l) = raw[i];
-                } else if (kind == 2) {
-                    *reinterpret_cast<uint4*>(a.V + (((size_t)b * a.Hkv + h0 + h) * a.ldL + start + t0 + tl) * D + 8 * l) =
-                        raw[i];
-                } else {
-                    const uint32_t u[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+                if (kind == 1) {
+                    uint16_t* ta = tile[h] + A * kTilePitch + tl;
+                    uint16_t* tb = tile[h] + B * kTilePitch + tl;
+                    const uint32_t ua[4] = {ra[i].x, ra[i].y, ra[i].z, ra[i].w};
+                    const uint32_t ub[4] = {rb[i].x, rb[i].y, rb[i].z, rb[i].w};
 #pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        tile[h][(8 * l + e) * kTilePitch + tl] = (uint16_t)(u[e >> 1] >> (16 * (e & 1)));
+                    for (int e = 0; e < 8; ++e) {
+                        ta[e * kTilePitch] = (uint16_t)(ua[e >> 1] >> (16 * (e & 1)));
+                        tb[e * kTilePitch] = (uint16_t)(ub[e >> 1] >> (16 * (e & 1)));
+                    }
+                } else {
+                    uint16_t* dst = kind == 0 ? a.Q + (((size_t)b * a.Hq + h0 + h) * a.T + t0 + tl) * D
+                                              : a.V + (((size_t)b * a.Hkv + h0 + h) * a.ldL + start + t0 + tl) * D;
+                    *reinterpret_cast<uint4*>(dst + A) = ra[i];
+                    *reinterpret_cast<uint4*>(dst + B) = rb[i];
                 }
             }
         }
@@ -204,24 +268,17 @@ __global__ void __launch_bounds__(kRopeThreads) qkv_rope_kernel(const RopeArgs a
     uint16_t* Kg = a.Kt + ((size_t)b * a.Hkv + h0) * D * (size_t)a.ldL;
     for (int i = tid; i < nh * D * np; i += kRopeThreads) {
         const int hj = i / np, p = p0 + i % np;  // hj: head * D + dim, a row of the cache
-        const uint16_t* t = tile[hj >> 7] + (hj & (D - 1)) * kTilePitch;
-        uint16_t v[8];
-        bool all = true, ok[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const int tl = 8 * p + e - s0;
-            ok[e] = tl >= 0 && tl < nt && pos_s[min(max(tl, 0), kRopeTokens - 1)] >= 0;
-            all = all && ok[e];
-            v[e] = ok[e] ? t[tl] : (uint16_t)0;
-        }
+        const int tl = 8 * p - s0;
+        const uint16_t* t = tile[hj >> 7] + (hj & (D - 1)) * kTilePitch + tl;
         uint16_t* dst = Kg + (size_t)hj * a.ldL + 8 * p;
-        if (all) {
-            *reinterpret_cast<uint4*>(dst) = make_uint4(v[0] | ((uint32_t)v[1] << 16), v[2] | ((uint32_t)v[3] << 16),
-                                                        v[4] | ((uint32_t)v[5] << 16), v[6] | ((uint32_t)v[7] << 16));
-        } else {
+        if (tl >= 0 && tl + 8 <= nt && !holes) {
+            uint32_t v[4];
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                if (ok[e]) dst[e] = v[e];
+            for (int e = 0; e < 4; ++e) v[e] = t[2 * e] | ((uint32_t)t[2 * e + 1] << 16);
+            *reinterpret_cast<uint4*>(dst) = make_uint4(v[0], v[1], v[2], v[3]);
+        } else {
+            for (int e = max(0, -tl); e < 8 && tl + e < nt; ++e)
+                if (pos_s[tl + e] >= 0) dst[e] = t[e];
         }
     }
 }
