@@ -368,7 +368,7 @@ rmm_status rmm_heads_to_tokens(const void* O, int Hq, int T, int d, void* A, rmm
  *   Yv bf16 [B*T, Hkv*d] -> V [B, Hkv, ldL, d] at slot start + t
  * start = lens[b], or L0 for every sequence with lens NULL (then L0 >= 0 and
  * L0 + T <= ldL); pos = start + t, or with parents start + the node's depth.
- * Sums, angles and products are fp32 (angles fp64 until reduced), each output
+ * Sums and products are fp32 (angles in 64-bit fixed point until reduced), each output
  * is rounded once.  Empty slots and absent nodes write nothing; other cache
  * positions are not touched.  Requires d == 128, rot % 16 == 0 and rot <= d,
  * ldL % 8 == 0, T <= 2^20, 16-byte aligned bf16 pointers. */
