@@ -2,11 +2,23 @@
 //   y_i = e^((x_i - M) / t) / sum_j e^((x_j - M) / t),   M = max_j x_j
 // bf16 in, fp32 out; at temperature 0 the limit, 1 at the lowest index of M.
 //
-// Memory bound: 2 bytes read and 4 written per element.  A row belongs to a
-// cluster of 1, 2, 4 or 8 CTAs, each of which keeps its part of the row in
-// registers between the passes, so the row is read once.  Each CTA forms its
-// own maximum and its sum relative to that; one exchange of these pairs through
-// distributed shared memory gives the row's maximum and sum.
+// Memory bound by its data, 2 bytes read and 4 written per element; two kernels
+// form the maximum and the sum relative to it with one exchange between the CTAs of
+// a row, as pairs that merge exactly like a running maximum and sum.
+//   softmax_kernel       a row in the registers of a cluster of 1, 2, 4 or 8 CTAs,
+//                        read once: the shortest way for one row, but every CTA of
+//                        the SM loads, exchanges and stores at the same time
+//   softmax_rows_kernel  a row in parts over 4 small CTAs, read twice (the second
+//                        time from L2): five CTAs per SM in different phases
+// Measured, us for (rows, V), registers against parts:
+//   (16, 32000) 5.5 4.2   (32, 16384) 4.5 4.1   (32, 131072) 12.9 14.6
+//   (64, 4096) 2.4 3.8    (64, 8192) 4.1 4.0    (64, 32000) 13.6 7.3
+//   (512, 8192) 15.1 17.3 (512, 16384) 29.6 20.9   (512, 131072) 158 97
+// so parts are taken from 32 rows of 16384 logits on, where rows start on 16-byte
+// boundaries.  (512, 131072) moves 4.15 TB/s of its 403 MB; the two exponentials
+// per element take 35 us of it, the wait for the cluster and uneven phases the rest.
+// A wave of resident clusters over many rows (169 us) and 8 or 16 vectors in
+// flight per thread (109, 126) were slower.
 #include <math.h>
 
 #include "rmm_common.cuh"
@@ -17,6 +29,10 @@ namespace rmm {
 namespace {
 
 constexpr int kThreads = 512;
+// softmax_rows_kernel: when it is taken, its threads, CTAs per SM, CTAs per row and
+// vectors in flight (us at 512 x 131072: 97; 6 CTAs 109, 2 vectors 105, 8 parts 111)
+constexpr int kManyRows = 32, kLongRow = 16384;
+constexpr int kRowThreads = 256, kRowCtas = 5, kParts = 4, kRowFly = 4;
 constexpr float kLog2e = 1.4426950408889634f;
 
 __device__ __forceinline__ float ld_shared_cluster_f32(uint32_t addr) {
@@ -25,12 +41,19 @@ __device__ __forceinline__ float ld_shared_cluster_f32(uint32_t addr) {
     return v;
 }
 
+// 2^x, -inf gives 0 (about 2 ulp)
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 // Merge (m, s): the maximum of two parts, the sum relative to it.  Parts without
 // a finite or infinite element have m = -inf and s = 0.
 __device__ __forceinline__ void merge(float& m, float& s, float m2, float s2, float c) {
     const float mm = fmaxf(m, m2);
-    const float a = m == mm ? s : s * exp2f((m - mm) * c);
-    const float b = m2 == mm ? s2 : s2 * exp2f((m2 - mm) * c);
+    const float a = m == mm ? s : s * ex2((m - mm) * c);
+    const float b = m2 == mm ? s2 : s2 * ex2((m2 - mm) * c);
     m = mm;
     s = a + b;
 }
@@ -125,7 +148,7 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
         for (int i = 0; i < NV; ++i)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) s += exp2f((at(i, e) - m) * c);
+            for (int e = 0; e < 8; ++e) s += ex2((at(i, e) - m) * c);
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
@@ -151,7 +174,7 @@ __global__ void __launch_bounds__(kThreads)
         if (e0 >= V) continue;
         float p[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) p[e] = m > -INFINITY ? exp2f((at(i, e) - m) * c) * inv : 0.0f;
+        for (int e = 0; e < 8; ++e) p[e] = m > -INFINITY ? ex2((at(i, e) - m) * c) * inv : 0.0f;
         if (wide_y && e0 + 8 <= V) {
             *reinterpret_cast<float4*>(y + e0) = make_float4(p[0], p[1], p[2], p[3]);
             *reinterpret_cast<float4*>(y + e0 + 4) = make_float4(p[4], p[5], p[6], p[7]);
@@ -161,6 +184,105 @@ __global__ void __launch_bounds__(kThreads)
                 if (e0 + e < V) y[e0 + e] = p[e];
         }
     }
+}
+
+__device__ __forceinline__ __nv_bfloat162 pair(uint32_t w) { return *reinterpret_cast<const __nv_bfloat162*>(&w); }
+
+// A part of a row per CTA (a cluster of kParts), read twice: for the maximum and the
+// sum, then for the probabilities.  Stores bypass the caches' lasting part so that the
+// second read still hits L2 (107 us without, 98 with).
+__global__ void __launch_bounds__(kRowThreads, kRowCtas)
+    softmax_rows_kernel(const uint16_t* X, int V, int64_t ldx, float c, float* Y, int64_t ldy) {
+    __shared__ float red_m[kRowThreads / 32], red_s[kRowThreads / 32];
+    __shared__ float part[2];
+    constexpr int kFly = kRowFly;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int64_t row = blockIdx.x / kParts;
+    const int rank = blockIdx.x % kParts;
+    const int vecs = V / 8, per = (vecs / kParts + 32) & ~31;
+    const int lo = rank * per, hi = min(vecs, lo + per);
+    const bool tail = rank == kParts - 1 && vecs * 8 + tid < V;  // the last, partial vector
+    const uint16_t* x = X + row * ldx;
+    float* y = Y + row * ldy;
+    pdl_wait();
+    pdl_launch_dependents();
+    auto at = [](const uint4& r, int e) -> float {
+        const uint32_t w = e < 2 ? r.x : e < 4 ? r.y : e < 6 ? r.z : r.w;
+        return __uint_as_float((e & 1) ? w & 0xFFFF0000u : w << 16);
+    };
+    float m = -INFINITY, s = 0.f;
+    for (int i0 = lo + tid; i0 < hi; i0 += kFly * kRowThreads) {
+        uint4 r[kFly];
+#pragma unroll
+        for (int i = 0; i < kFly; ++i)
+            r[i] = i0 + i * kRowThreads < hi ? *reinterpret_cast<const uint4*>(x + (int64_t)(i0 + i * kRowThreads) * 8)
+                                          : make_uint4(0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u);
+        // the maximum in pairs, as bf16 (exact)
+        __nv_bfloat162 top = pair(r[0].x);
+#pragma unroll
+        for (int i = 0; i < kFly; ++i) {
+            top = __hmax2(top, __hmax2(pair(r[i].x), pair(r[i].y)));
+            top = __hmax2(top, __hmax2(pair(r[i].z), pair(r[i].w)));
+        }
+        const float mm = fmaxf(m, fmaxf(__low2float(top), __high2float(top)));
+        if (mm > m) {
+            s *= ex2((m - mm) * c);
+            m = mm;
+        }
+        if (m > -INFINITY) {
+#pragma unroll
+            for (int i = 0; i < kFly; ++i)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) s += ex2((at(r[i], e) - m) * c);
+        }
+    }
+    if (tail) {
+        const uint32_t v = x[vecs * 8 + tid];
+        merge(m, s, __uint_as_float(v << 16), v == 0xFF80u ? 0.f : 1.f, c);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        const float m2 = __shfl_xor_sync(0xffffffffu, m, o), s2 = __shfl_xor_sync(0xffffffffu, s, o);
+        merge(m, s, m2, s2, c);
+    }
+    if (lane == 0) red_m[warp] = m, red_s[warp] = s;
+    __syncthreads();
+    m = red_m[lane & (kRowThreads / 32 - 1)], s = red_s[lane & (kRowThreads / 32 - 1)];
+#pragma unroll
+    for (int o = kRowThreads / 64; o > 0; o >>= 1) {
+        const float m2 = __shfl_xor_sync(0xffffffffu, m, o), s2 = __shfl_xor_sync(0xffffffffu, s, o);
+        merge(m, s, m2, s2, c);
+    }
+    if (tid == 0) part[0] = m, part[1] = s;
+    cluster_sync();
+    m = -INFINITY, s = 0.f;
+#pragma unroll
+    for (int j = 0; j < kParts; ++j)
+        merge(m, s, ld_shared_cluster_f32(mapa_shared(smem_addr(&part[0]), j)),
+              ld_shared_cluster_f32(mapa_shared(smem_addr(&part[1]), j)), c);
+    const float inv = 1.0f / s;
+    const bool any = m > -INFINITY;
+    for (int i0 = lo + tid; i0 < hi; i0 += kFly * kRowThreads) {
+        uint4 r[kFly];
+#pragma unroll
+        for (int i = 0; i < kFly; ++i)
+            if (i0 + i * kRowThreads < hi) r[i] = *reinterpret_cast<const uint4*>(x + (int64_t)(i0 + i * kRowThreads) * 8);
+#pragma unroll
+        for (int i = 0; i < kFly; ++i) {
+            if (i0 + i * kRowThreads >= hi) break;
+            float p[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) p[e] = any ? ex2((at(r[i], e) - m) * c) * inv : 0.0f;
+            float4* d = reinterpret_cast<float4*>(y + (int64_t)(i0 + i * kRowThreads) * 8);
+            __stcs(d, make_float4(p[0], p[1], p[2], p[3]));
+            __stcs(d + 1, make_float4(p[4], p[5], p[6], p[7]));
+        }
+    }
+    if (tail) {
+        const float v = __uint_as_float((uint32_t)x[vecs * 8 + tid] << 16);
+        y[vecs * 8 + tid] = any ? ex2((v - m) * c) * inv : 0.0f;
+    }
+    cluster_sync();  // no CTA leaves while another still reads its pair
 }
 
 template <int NV>
@@ -191,6 +313,24 @@ cudaError_t launch(const uint16_t* X, int rows, int V, int64_t ldx, float temper
 cudaError_t launch_softmax(const uint16_t* X, int rows, int V, int64_t ldx, float temperature, float* Y, int64_t ldy,
                            cudaStream_t stream) {
     const int vecs = (V + 7) / 8;
+    const bool aligned = (reinterpret_cast<uintptr_t>(X) & 15) == 0 && ldx % 8 == 0 &&
+                         (reinterpret_cast<uintptr_t>(Y) & 15) == 0 && ldy % 4 == 0;
+    if (aligned && temperature != 0.0f && rows >= kManyRows && V >= kLongRow) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)rows * kParts);
+        cfg.blockDim = dim3(kRowThreads);
+        cfg.stream = stream;
+        cudaLaunchAttribute attr[2];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        attr[1].id = cudaLaunchAttributeClusterDimension;
+        attr[1].val.clusterDim.x = kParts;
+        attr[1].val.clusterDim.y = 1;
+        attr[1].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 2;
+        return cudaLaunchKernelEx(&cfg, softmax_rows_kernel, X, V, ldx, kLog2e / temperature, Y, ldy);
+    }
     int nc = 1;
     while (nc < 8 && vecs > nc * kThreads) nc *= 2;
     const int nv = (vecs + nc * kThreads - 1) / (nc * kThreads);
