@@ -134,13 +134,19 @@ def lib() -> ctypes.CDLL:
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
+
+
+# the handle of a device's current stream without a torch.cuda.Stream around it (0.3 us instead of 3.4)
+_current_handle = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _stream(stream):
-    if stream is None:
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream)
+    if stream is not None:
+        return stream.cuda_stream
+    if _current_handle is None:
+        return torch.cuda.current_stream().cuda_stream
+    return _current_handle(torch.cuda.current_device())
 
 
 def _opt(o):
@@ -165,7 +171,7 @@ def _need(t, name, dtype=torch.bfloat16, shape=None, min_numel=None):
         return
     if t.dtype != dtype or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape and tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     if min_numel is not None and t.numel() < min_numel:
         raise ValueError(f"{name} holds {t.numel()} elements, needs at least {min_numel}")
@@ -544,11 +550,14 @@ def _here(**tensors):
     for name, t in tensors.items():
         if t is None:
             continue
+        d = t.get_device()
+        if d == dev:
+            continue
         if not t.is_cuda:
             raise ValueError(f"{name} must be a CUDA tensor")
         if dev is None:
             dev = torch.cuda.current_device()
-        if t.device.index != dev:
+        if d != dev:
             raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
 
 
@@ -646,12 +655,21 @@ def _rows(t, name, dtype, rows=None, V=None):
     """A 2-D tensor whose rows are contiguous (their stride may be larger than V): its row stride."""
     if t.dtype != dtype or t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
         raise ValueError(f"{name} must be a 2-D {dtype} tensor with contiguous rows")
-    if rows is not None and tuple(t.shape) != (rows, V):
+    if rows is not None and t.shape != (rows, V):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(rows, V)}")
     ld = t.stride(0) if t.shape[0] > 1 else t.shape[1]
     if ld < t.shape[1]:
         raise ValueError(f"{name} has overlapping rows")
     return ld
+
+
+def _node_rows(t, name, B, T, V):
+    """A row per node, [B, T, V] contiguous or [B*T, V] with a row stride: the stride."""
+    if t.dtype == torch.float32 and t.is_contiguous() and t.shape == (B, T, V):
+        return V
+    if t.dim() == 3 and t.is_contiguous():
+        t = t.flatten(0, 1)
+    return _rows(t, name, torch.float32, B * T, V)
 
 
 def rmm_softmax(X: torch.Tensor, temperature: float = 1.0, Y: torch.Tensor | None = None, stream=None) -> torch.Tensor:
@@ -679,15 +697,9 @@ def rmm_tree_verify(P: torch.Tensor, tokens: torch.Tensor, parents: torch.Tensor
     _need(tokens, "tokens", torch.int32)
     _need(parents, "parents", torch.int32, shape=(B, T))
     _need(u, "u", torch.float32, shape=(B, T))
-    if P.dim() == 3:
-        P = P.flatten(0, 1) if P.is_contiguous() else P
     V = P.shape[-1]
-    ldp = _rows(P, "P", torch.float32, B * T, V)
-    ldq = 0
-    if Qd is not None:
-        if Qd.dim() == 3:
-            Qd = Qd.flatten(0, 1) if Qd.is_contiguous() else Qd
-        ldq = _rows(Qd, "Qd", torch.float32, B * T, V)
+    ldp = _node_rows(P, "P", B, T, V)
+    ldq = 0 if Qd is None else _node_rows(Qd, "Qd", B, T, V)
     _need(path, "path", torch.int32, shape=(B, T))
     _need(emitted, "emitted", torch.int32, shape=(B, T))
     _need(count, "count", torch.int32, shape=(B,))
@@ -712,17 +724,21 @@ def rmm_cache_keep(caches, lens: torch.Tensor, path: torch.Tensor, count: torch.
     if not caches:
         raise ValueError("no cache given")
     B, Hkv, d, ldL = _caches(*caches[0])
+    bf16, k_shape, v_shape, device = torch.bfloat16, (B, Hkv, d, ldL), (B, Hkv, ldL, d), path.get_device()
     for Kt, V in caches:
-        _need(Kt, "Kt", shape=(B, Hkv, d, ldL))
-        _need(V, "V", shape=(B, Hkv, ldL, d))
-        _here(Kt=Kt, V=V)
+        if not (Kt.dtype is bf16 and V.dtype is bf16 and Kt.shape == k_shape and V.shape == v_shape
+                and Kt.is_contiguous() and V.is_contiguous()
+                and Kt.get_device() == device and V.get_device() == device):
+            _need(Kt, "Kt", shape=k_shape)
+            _need(V, "V", shape=v_shape)
+            _here(Kt=Kt, V=V, path=path)
     _dims(path, "path", 2)
     T = path.shape[1]
     _need(path, "path", torch.int32, shape=(B, T))
     _need(lens, "lens", torch.int32, shape=(B,))
     _need(count, "count", torch.int32, shape=(B,))
     _need(lens_out, "lens_out", torch.int32, shape=(B,))
-    _here(lens=lens, path=path, count=count, lens_out=lens_out)
+    _here(path=path, lens=lens, count=count, lens_out=lens_out)  # and with path the caches
     if lens_out is None:
         lens_out = _new((B,), torch.int32, lens, stream)
     n = len(caches)
