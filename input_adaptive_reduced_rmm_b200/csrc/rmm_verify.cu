@@ -14,13 +14,18 @@
 // R and every sum are fp64: a token changes where a sum passes a random number,
 // and 1e-16 of the mass keeps that border where the definition has it.
 //
-// One cluster of 8 CTAs per sequence.  The tests need one probability each,
-// fetched up front for all nodes; a pass over the vocabulary runs only for a
-// rejection, and for the next token where the walk ends on an accepted node.
-// R is never stored: a pass forms it again from the rows and the masses of the
-// rejections before it.  Each pass leaves the sum of every warp's own range of
-// indices, so the next token is found by walking the 8 CTAs' sums, 16 warps'
-// sums and one warp's range.
+// One cluster of 8 CTAs per sequence; each of its 128 warps has a contiguous range
+// of the vocabulary.  The tests need one probability each, fetched up front for all
+// nodes; the rows themselves are read only at a node where a child is rejected, and
+// at the last node, once: R (fp64) and the draft's row then stay in registers for
+// the node's further rejections and the search of the next token.  A vocabulary
+// above 131072 does not fit there; its passes read the rows again and repeat the
+// rejections so far.  A pass sends every warp's sum to all 8 CTAs, so one barrier of
+// the cluster gives each of them the total and, for the next token, the place.
+// Latency bound: a node's rows take one exposed read, a rejection one barrier of the
+// cluster.  16 trees of 32 nodes over 131072 tokens take 28 us (57 us when every
+// pass read its rows again and the search walked 32 indices at a time), one chain of
+// 8 over 32000 tokens 8 us (18 us).
 #include <math.h>
 
 #include "rmm_common.cuh"
@@ -34,11 +39,11 @@ namespace {
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kCtas = 8;
+constexpr int kAll = kCtas * kWarps;  // warps of a sequence
+constexpr int kStep = 128;            // indices a warp takes at once, 4 per lane
 
-__device__ __forceinline__ double ld_shared_cluster_f64(uint32_t addr) {
-    double v;
-    asm volatile("ld.shared::cluster.f64 %0, [%1];" : "=d"(v) : "r"(addr) : "memory");
-    return v;
+__device__ __forceinline__ void st_shared_cluster_f64(uint32_t addr, double v) {
+    asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(addr), "d"(v) : "memory");
 }
 
 __device__ __forceinline__ double warp_sum(double v) {
@@ -50,32 +55,121 @@ __device__ __forceinline__ double warp_sum(double v) {
 // a probability as the walk reads it: NaN and negative values count as 0
 __device__ __forceinline__ double prob(float p) { return p > 0.0f ? (double)p : 0.0; }
 
-struct Walk {
-    double mass[kTreeMax + 1];  // Z before each rejection at the current node, then the current Z
-    int rejected[kTreeMax];     // their tokens
+// the inclusive sum over the lanes up to this one
+__device__ __forceinline__ double warp_prefix(double v, int lane) {
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const double y = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += y;
+    }
+    return v;
+}
+
+// Rejections at the current node: the mass before each (mass[0] is 1) and its token.
+struct Rejections {
+    double mass[kTreeMax];
+    int token[kTreeMax];
 };
 
-// R at index i, given the rows' values there and the rejections so far.
-__device__ __forceinline__ double remaining(double r, double q, int i, bool drawn, int n, const Walk& w) {
+// R at one index of token x after n rejections, from the rows' values there.
+__device__ __forceinline__ double remaining(double r, double q, int x, bool drawn, int n, const Rejections& w) {
     if (drawn) {
         for (int j = 0; j < n; ++j) r = fmax(r - w.mass[j] * q, 0.0);
     } else {
         for (int j = 0; j < n; ++j)
-            if (w.rejected[j] == i) r = 0.0;
+            if (w.token[j] == x) r = 0.0;
     }
     return r;
 }
 
+// NV steps of a warp's range, as a lane holds them: 4 indices of each.
+template <int NV>
+struct Tile {
+    double r[NV][4];
+    alignas(16) float q[NV][4];
+
+    __device__ __forceinline__ void load(const float* p, const float* dq, int first, int hi, bool wide) {
+        wide = wide && first + (NV - 1) * kStep + 4 <= hi;
+        if (dq) {
+            if (wide) {
+#pragma unroll
+                for (int i = 0; i < NV; ++i)
+                    *reinterpret_cast<float4*>(q[i]) = *reinterpret_cast<const float4*>(dq + first + i * kStep);
+            } else {
+#pragma unroll
+                for (int i = 0; i < NV; ++i) fetch(q[i], dq, first + i * kStep, hi);
+            }
+        }
+        constexpr int kFly = NV < 4 ? NV : 4;
+#pragma unroll
+        for (int h = 0; h < NV; h += kFly) {
+            alignas(16) float a[kFly][4];
+#pragma unroll
+            for (int i = 0; i < kFly; ++i) {
+                if (wide)
+                    *reinterpret_cast<float4*>(a[i]) = *reinterpret_cast<const float4*>(p + first + (h + i) * kStep);
+                else
+                    fetch(a[i], p, first + (h + i) * kStep, hi);
+            }
+#pragma unroll
+            for (int i = 0; i < kFly; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) r[h + i][e] = prob(a[i][e]);
+        }
+    }
+    static __device__ __forceinline__ void fetch(float (&d)[4], const float* s, int x, int hi) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) d[e] = x + e < hi ? s[x + e] : 0.0f;
+    }
+    __device__ __forceinline__ void reject(bool drawn, double mass, int token, int first) {
+        if (drawn) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) r[i][e] = fmax(r[i][e] - mass * prob(q[i][e]), 0.0);
+        } else {
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (first + i * kStep + e == token) r[i][e] = 0.0;
+        }
+    }
+    __device__ __forceinline__ double step_sum(int i) const {
+        return (r[i][0] + r[i][1]) + (r[i][2] + r[i][3]);
+    }
+    __device__ __forceinline__ double sum() const {
+        double s = 0.0;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) s += step_sum(i);
+        return s;
+    }
+};
+
+// The place of the first of the lanes' values at which the running sum, from base on,
+// passes goal; the last one with mass if none does; -1 without any.  base becomes the
+// sum before that place.
+__device__ __forceinline__ int place(double v, double goal, int lane, double& base) {
+    const double inc = warp_prefix(v, lane);
+    const unsigned has = __ballot_sync(0xffffffffu, v > 0.0);
+    const unsigned over = __ballot_sync(0xffffffffu, v > 0.0 && base + inc > goal);
+    if (!has) return -1;
+    const int at = over ? __ffs(over) - 1 : 31 - __clz(has);
+    const double upto = __shfl_sync(0xffffffffu, inc, at > 0 ? at - 1 : 0);
+    if (at > 0) base += upto;
+    return at;
+}
+
+// kResident: a warp's range is one tile, kept from pass to pass.
+template <int NV, bool kResident>
 __global__ void __launch_bounds__(kThreads)
-    tree_verify_kernel(const float* P, int64_t ldp, const float* Qd, int64_t ldq, int V,
-                       int T, const int32_t* tokens, const int32_t* parents,
-                       const float* u, int32_t* path, int32_t* emitted,
-                       int32_t* count, int per_warp, int wide) {
+    tree_verify_kernel(const float* P, int64_t ldp, const float* Qd, int64_t ldq, int V, int T, const int32_t* tokens,
+                       const int32_t* parents, const float* u, int32_t* path, int32_t* emitted, int32_t* count,
+                       int per_warp, bool wide) {
     __shared__ int par[kTreeMax], tok[kTreeMax], way[kTreeMax];
     __shared__ double pv[kTreeMax], qv[kTreeMax], uv[kTreeMax];
-    __shared__ Walk w;
-    __shared__ double warp_part[kWarps];
-    __shared__ double cta_part[2];
+    __shared__ Rejections w;
+    __shared__ double part[2][kAll];  // [pass parity]: the sums of all warps of the sequence
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int b = blockIdx.x / kCtas, rank = blockIdx.x % kCtas;
     const bool drawn = Qd != nullptr;
@@ -91,7 +185,8 @@ __global__ void __launch_bounds__(kThreads)
         qv[tid] = ok && drawn ? prob(Qd[(node0 + p) * ldq + x]) : 1.0;
         uv[tid] = (double)u[node0 + tid];
     }
-    __syncthreads();
+    if (tid == 0) way[0] = 0, w.mass[0] = 1.0;
+    cluster_sync();  // every CTA of the cluster runs, its shared memory can be written
     if (par[0] != -1) {  // an empty slot of the batch
         if (rank == 0) {
             if (tid < T) path[node0 + tid] = emitted[node0 + tid] = -1;
@@ -100,96 +195,103 @@ __global__ void __launch_bounds__(kThreads)
         return;  // all 8 CTAs of the cluster
     }
 
-    const int lo = (rank * kWarps + warp) * per_warp, hi = min(V, lo + per_warp);  // this warp's indices
+    const int me = rank * kWarps + warp;
+    // this warp's indices; ranges past the end are empty (V <= 2^24, so the product fits)
+    const int lo = me * per_warp, hi = min(V, lo + per_warp), first = lo + lane * 4;
+    Tile<NV> tile;
     int v = 0, n = 0, found = 1, passes = 0;
     double total = 0.0;
-    bool summed = false;  // warp_part and total hold the sums of the current R
+    bool loaded = false;  // the tile holds R of node v after n rejections
+    bool summed = false;  // part and total hold the sums of the current R
 
-    // the sum of R over the vocabulary, rejections 0 .. n-1 applied
-    auto pass = [&](int n_rej) -> double {
+    auto fill = [&](int start, int n_rej) {
         const float* p = P + (node0 + v) * ldp;
-        const float* q = drawn ? Qd + (node0 + v) * ldq : p;
+        const float* q = drawn ? Qd + (node0 + v) * ldq : nullptr;
+        tile.load(p, q, start, hi, wide);
+        for (int j = 0; j < n_rej; ++j) tile.reject(drawn, w.mass[j], w.token[j], start);
+    };
+    // the sum of R over the vocabulary, rejections 0 .. n_rej-1 applied
+    auto pass = [&](int n_rej) -> double {
         double acc = 0.0;
-        if (wide) {
-            for (int i = lo + lane * 4; i < hi; i += 128) {
-                if (i + 4 <= hi) {
-                    const float4 a = *reinterpret_cast<const float4*>(p + i);
-                    const float4 c = drawn ? *reinterpret_cast<const float4*>(q + i) : a;
-                    acc += remaining(prob(a.x), prob(c.x), i, drawn, n_rej, w);
-                    acc += remaining(prob(a.y), prob(c.y), i + 1, drawn, n_rej, w);
-                    acc += remaining(prob(a.z), prob(c.z), i + 2, drawn, n_rej, w);
-                    acc += remaining(prob(a.w), prob(c.w), i + 3, drawn, n_rej, w);
-                } else {
-                    for (int e = i; e < hi; ++e) acc += remaining(prob(p[e]), prob(q[e]), e, drawn, n_rej, w);
-                }
+        if (kResident) {
+            if (!loaded) {
+                fill(first, n_rej);
+            } else if (n_rej > n) {
+                tile.reject(drawn, w.mass[n], w.token[n], first);
             }
+            loaded = true;
+            acc = tile.sum();
         } else {
-            for (int i = lo + lane; i < hi; i += 32) acc += remaining(prob(p[i]), prob(q[i]), i, drawn, n_rej, w);
+            for (int s = first; s - lane * 4 < hi; s += NV * kStep) {
+                fill(s, n_rej);
+                acc += tile.sum();
+            }
         }
         acc = warp_sum(acc);
-        __syncthreads();  // the sums of the pass before have been read
-        if (lane == 0) warp_part[warp] = acc;
-        __syncthreads();
-        double s = 0.0;
-        for (int i = 0; i < kWarps; ++i) s += warp_part[i];
-        double* slot = &cta_part[passes & 1];  // read by the cluster until its next barrier
-        if (tid == 0) *slot = s;
+        double* const slot = part[passes & 1];  // the other one may still be read by a slower CTA
+        if (lane < kCtas) st_shared_cluster_f64(mapa_shared(smem_addr(&slot[me]), lane), acc);
         cluster_sync();
         double t = 0.0;
-        for (int j = 0; j < kCtas; ++j) t += ld_shared_cluster_f64(mapa_shared(smem_addr(slot), j));
+#pragma unroll
+        for (int i = 0; i < kAll / 32; ++i) t += slot[lane * (kAll / 32) + i];
         ++passes;
-        return t;
+        return warp_sum(t);
     };
 
-    if (tid == 0) {
-        way[0] = 0;
-        w.mass[0] = 1.0;
-    }
-    __syncthreads();
     // children after their parents and in order: one sweep over the nodes walks the tree;
-    // every thread of the cluster takes the same steps on the same values
-    for (int c = 1; c < T; ++c) {
-        if (par[c] != v) continue;
-        const double r = remaining(pv[c], qv[c], tok[c], drawn, n, w);
-        if (uv[c] * qv[c] * w.mass[n] < r) {
-            v = c;
-            n = 0;
-            summed = false;
-            __syncthreads();
-            if (tid == 0) {
-                way[found] = c;
-                w.mass[0] = 1.0;
+    // every thread of the cluster takes the same steps on the same values.  c = T: the sums
+    // of the last node, where its rejections have not left them.
+    for (int c = 1; c <= T; ++c) {
+        if (c < T) {
+            if (par[c] != v) continue;
+            const double r = remaining(pv[c], qv[c], tok[c], drawn, n, w);
+            if (uv[c] * qv[c] * w.mass[n] < r) {
+                if (tid == 0) way[found] = c;
+                v = c;
+                ++found;
+                n = 0;
+                loaded = summed = false;
+                continue;
             }
-            ++found;
+            __syncthreads();  // the tests that read the list are done
+            if (tid == 0) w.token[n] = tok[c];
+            __syncthreads();
+        } else if (summed) {
+            break;
+        }
+        const double t = pass(c < T ? n + 1 : n);
+        if (c == T) {
+            total = t;
+        } else if (t > 0.0) {
+            ++n;
+            total = t;
+            summed = true;
+            if (tid == 0 && n < kTreeMax) w.mass[n] = t;
             __syncthreads();
         } else {
-            __syncthreads();
-            if (tid == 0) w.rejected[n] = tok[c];
-            __syncthreads();
-            const double t = pass(n + 1);
-            if (t > 0.0) {
-                ++n;
-                total = t;
-                summed = true;
-                if (tid == 0) w.mass[n] = t;
-                __syncthreads();
-            } else {
-                summed = false;  // the draft covered all that was left: the rejection takes nothing away
-            }
+            loaded = summed = false;  // the draft covered all that was left: the rejection takes nothing away
         }
     }
-    if (!summed) total = pass(n);
 
-    // the next token: the CTA, then the warp, then the index where the running sum passes u_0
-    double goal = (uv[0] > 0.0 ? uv[0] : 0.0) * total;
-    const uint32_t my_slot = smem_addr(&cta_part[(passes - 1) & 1]);
-    int owner = -1;
-    double before = 0.0, run = 0.0;
-    for (int j = 0; j < kCtas; ++j) {
-        const double s = ld_shared_cluster_f64(mapa_shared(my_slot, j));
-        if (s > 0.0 && !(owner >= 0 && run > goal)) owner = j, before = run;  // the last one with mass if none passes
-        run += s;
+    // the next token: the warp, then its step, lane and index where the running sum passes u_0
+    const double goal = (uv[0] > 0.0 ? uv[0] : 0.0) * total;
+    const double* slot = part[(passes - 1) & 1];
+    double base = 0.0, mine = 0.0;
+#pragma unroll
+    for (int i = 0; i < kAll / 32; ++i) mine += slot[lane * (kAll / 32) + i];
+    int owner = place(mine, goal, lane, base);
+    if (owner >= 0) {
+        int pick = -1;
+        double upto = base, before = base;
+        for (int i = 0; i < kAll / 32; ++i) {
+            const double s = slot[owner * (kAll / 32) + i];
+            if (s > 0.0 && !(pick >= 0 && upto > goal)) pick = i, before = upto;  // the last one with mass if none passes
+            upto += s;
+        }
+        owner = owner * (kAll / 32) + pick;
+        base = before;
     }
+    __syncthreads();  // way is written
     if (rank == 0) {
         if (tid < T) {
             path[node0 + tid] = tid < found ? way[tid] : -1;
@@ -200,43 +302,57 @@ __global__ void __launch_bounds__(kThreads)
         }
         if (tid == 0) count[b] = found;
     }
-    if (rank == owner) {
-        int ow = -1;
-        double wb = before, wr = before;
-        for (int i = 0; i < kWarps; ++i) {
-            const double s = warp_part[i];
-            if (s > 0.0 && !(ow >= 0 && wr > goal)) ow = i, wb = wr;
-            wr += s;
+    if (me != owner) return;
+
+    int start = first;
+    if (!kResident) {  // the tile, the last one with mass if none passes
+        double run = base, before = base;
+        int held = -1;
+        bool over = false;
+        for (int s = first; !over && s - lane * 4 < hi; s += NV * kStep) {
+            fill(s, n);
+            const double t = warp_sum(tile.sum());
+            if (t > 0.0) start = held = s, before = run;
+            run += t;
+            over = t > 0.0 && run > goal;
         }
-        if (warp == ow) {
-            const float* p = P + (node0 + v) * ldp;
-            const float* q = drawn ? Qd + (node0 + v) * ldq : p;
-            double base = wb;
-            int last = -1;
-            bool done = false;
-            for (int i0 = lo; i0 < hi && !done; i0 += 32) {
-                const int i = i0 + lane;
-                const double x = i < hi ? remaining(prob(p[i]), prob(q[i]), i, drawn, n, w) : 0.0;
-                double inc = x;
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const double y = __shfl_up_sync(0xffffffffu, inc, o);
-                    if (lane >= o) inc += y;
-                }
-                const unsigned has = __ballot_sync(0xffffffffu, x > 0.0);
-                const unsigned over = __ballot_sync(0xffffffffu, x > 0.0 && base + inc > goal);
-                if (over) {
-                    last = i0 + __ffs(over) - 1;
-                    done = true;
-                } else if (has) {
-                    last = i0 + 31 - __clz(has);
-                }
-                base += __shfl_sync(0xffffffffu, inc, 31);
-            }
-            if (lane == 0) emitted[node0 + found - 1] = last;
-        }
+        base = before;
+        if (!over && held >= 0) fill(held, n);
     }
-    cluster_sync();  // no CTA leaves while another still reads its sums
+    double sums[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) sums[i] = warp_sum(tile.step_sum(i));
+    double run = base, x[4] = {0.0, 0.0, 0.0, 0.0};
+    int step = -1;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        if (sums[i] > 0.0 && !(step >= 0 && run > goal)) {
+            step = i, base = run;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[e] = tile.r[i][e];
+        }
+        run += sums[i];
+    }
+    const int at = place((x[0] + x[1]) + (x[2] + x[3]), goal, lane, base);
+    if (lane == at) {
+        int pick = 0;
+        run = base;
+        bool over = false;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            run += x[e];
+            if (x[e] > 0.0 && !over) pick = e, over = run > goal;
+        }
+        emitted[node0 + found - 1] = start + step * kStep + pick;
+    }
+}
+
+template <int NV, bool kResident>
+cudaError_t launch(cudaLaunchConfig_t& cfg, const float* P, int64_t ldp, const float* Qd, int64_t ldq, int V, int T,
+                   const int32_t* tokens, const int32_t* parents, const float* u, int32_t* path, int32_t* emitted,
+                   int32_t* count, int per_warp, bool wide) {
+    return cudaLaunchKernelEx(&cfg, tree_verify_kernel<NV, kResident>, P, ldp, Qd, ldq, V, T, tokens, parents, u, path, emitted,
+                              count, per_warp, wide);
 }
 
 }  // namespace
@@ -244,10 +360,10 @@ __global__ void __launch_bounds__(kThreads)
 cudaError_t launch_tree_verify(const float* P, int64_t ldp, const float* Qd, int64_t ldq, int B, int T, int V,
                                const int32_t* tokens, const int32_t* parents, const float* u, int32_t* path,
                                int32_t* emitted, int32_t* count, cudaStream_t stream) {
-    const int wide = (reinterpret_cast<uintptr_t>(P) & 15) == 0 && ldp % 4 == 0 &&
+    const bool wide = (reinterpret_cast<uintptr_t>(P) & 15) == 0 && ldp % 4 == 0 &&
                      (!Qd || ((reinterpret_cast<uintptr_t>(Qd) & 15) == 0 && ldq % 4 == 0));
-    // whole 128-index steps per warp, so that a warp's range starts on a 16-byte boundary
-    const int per_warp = ((V + kCtas * kWarps - 1) / (kCtas * kWarps) + 127) / 128 * 128;
+    // whole steps per warp, so that a warp's range starts on a 16-byte boundary
+    const int per_warp = ((V + kAll - 1) / kAll + kStep - 1) / kStep * kStep;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)B * kCtas);
     cfg.blockDim = dim3(kThreads);
@@ -261,8 +377,12 @@ cudaError_t launch_tree_verify(const float* P, int64_t ldp, const float* Qd, int
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, tree_verify_kernel, P, ldp, Qd, ldq, V, T, tokens, parents, u, path, emitted,
-                              count, per_warp, wide);
+    const auto run = per_warp <= kStep       ? launch<1, true>
+                     : per_warp <= 2 * kStep ? launch<2, true>
+                     : per_warp <= 4 * kStep ? launch<4, true>
+                     : per_warp <= 8 * kStep ? launch<8, true>
+                                             : launch<4, false>;
+    return run(cfg, P, ldp, Qd, ldq, V, T, tokens, parents, u, path, emitted, count, per_warp, wide);
 }
 
 }  // namespace rmm

@@ -358,6 +358,20 @@ def test_tree_verify(rmm, B, T, V, draft, fan, noise):
     check_verify(rmm, *verify_inputs(B, T, V, 31 * T + V, draft, fan, noise))
 
 
+@pytest.mark.parametrize("V", [131071, 131072, 131073, 300007])
+@pytest.mark.parametrize("draft", [True, False])
+def test_tree_verify_large_vocabularies(rmm, V, draft):
+    """Rows that just fill the registers of a sequence's CTAs and rows that do not fit there: rejections one
+    after the other at a node, the next token at both ends, mass in the last few tokens only."""
+    P, tokens, parents, u, Qd = verify_inputs(4, 6, V, V, draft, 5, 2.0, padded=False, roots=False)
+    parents[1:, 1:] = 0
+    u[1:, 1:] = 0.999
+    u[2, 0], u[3, 0] = 0.0, 1.0 - 2.0 ** -24
+    P[3, 0, : V - 3] = 0.0
+    want = check_verify(rmm, P, tokens, parents, u, Qd)
+    assert int(want[1][3, 0]) >= V - 3
+
+
 def test_tree_verify_walks_deep_and_rejects_often(rmm):
     """The inputs reach what they are for: long accepted paths and several rejections at a node."""
     *_, count = check_verify(rmm, *verify_inputs(64, 32, 100, 5, True, 2, 0.2, padded=False))
