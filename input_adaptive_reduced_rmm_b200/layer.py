@@ -10,10 +10,15 @@ The anatomy (RMSNorm, a residual stream through every block, a SwiGLU MLP)
 follows the 'Numerical Linear Algebra for LLMs' paper digest (ai-feeds.com),
 section 'Method: key modules'; the reduced products and the reduced QK^T
 follow the reduced-matrix-multiplication pages (input-adaptive slices of the
-contraction dimension kept at ratio r).  RoPE is not applied and the norm
-weights are 1.  Every op runs in this package's kernels through the C ABI;
+contraction dimension kept at ratio r).  The norm weights of the blocks are 1;
+per-head norms of q and k and the rotation by position are applied where their
+weights and frequencies are given.  Every op runs in this package's kernels through the C ABI;
 this module only sequences the calls and owns the buffers (PyTorch device
 memory).  Intermediates are bf16 between ops.
+
+Decoding with drafts: forward_tree scores a tree of drafted tokens behind the
+cache, decode_tree runs it through a stack of layers and an output head, keeps
+the branch that the model agrees with and drops the rest of the tree.
 """
 from __future__ import annotations
 
@@ -45,10 +50,19 @@ class LayerDims:
 
 
 class DecoderLayer:
-    """Weights pre-transposed once (W^T [in, out]); KV caches for max_len tokens."""
+    """Weights pre-transposed once (W^T [in, out]); KV caches for max_len tokens.
 
-    def __init__(self, dims: LayerDims, weights: dict, max_len: int, r: float, device):
+    q_norm, k_norm (bf16 [128], optional): weights of the RMS norms of each query and key head.
+    inv_freq (fp32 [rot/2], optional): the angle per position of each rotated pair of dims, (i, i + rot/2)
+    or, interleaved, (2i, 2i + 1)."""
+
+    def __init__(self, dims: LayerDims, weights: dict, max_len: int, r: float, device,
+                 q_norm: torch.Tensor | None = None, k_norm: torch.Tensor | None = None,
+                 inv_freq: torch.Tensor | None = None, interleaved: bool = False):
         self.d = dims
+        self.q_norm, self.k_norm, self.inv_freq = (None if t is None else t.to(device)
+                                                   for t in (q_norm, k_norm, inv_freq))
+        self.interleaved = bool(interleaved)
         self.r = float(r)
         self.dev = device
         self.Wt = {n: rmm.rmm_transpose_weight(weights[n].to(device)) for n in
@@ -85,11 +99,32 @@ class DecoderLayer:
         """x [T, H] bf16 at cache positions pos .. pos+T-1 (causal).  Returns the layer output.
         trace (optional) receives every intermediate and kept set; events (optional) receives
         (op name, start event, end event) per op."""
+        out = self._run(x, None, None, trace, events)
+        self.pos += x.shape[0]
+        return out
+
+    def forward_tree(self, x: torch.Tensor, parents: torch.Tensor | None = None, lens: torch.Tensor | None = None,
+                     trace: dict | None = None, events: list | None = None) -> torch.Tensor:
+        """x [T, H] bf16, the T <= 64 nodes of a tree of drafted tokens: parents int32 [T] (None: a chain) gives
+        each node's parent, smaller than its own number, -1 for the root.  A node's position is its depth past
+        the cache and it attends to the cache and its own ancestors.  Node t's key and value go to cache slot
+        pos + t; pos stays, so the next call overwrites them unless keep_path has moved some to their place.
+        lens (int32 [1], optional): pos on the device, where the caller has it."""
+        if lens is None:
+            lens = torch.full((1,), self.pos, dtype=torch.int32, device=self.dev)
+        return self._run(x, lens, parents, trace, events)
+
+    def _run(self, x, lens, parents, trace, events):
+        """One pass over the layer: causal rows at pos, or with lens the nodes of a tree behind it."""
         dm, T, r = self.d, x.shape[0], self.r
         L0 = self.pos
         if L0 + T > self.ldL:
             raise ValueError("KV cache full")
         H, F = dm.H, dm.F
+        tree = lens is not None
+        if parents is not None:
+            parents = parents.view(1, -1)
+        Kt, V = self.Kt.unsqueeze(0), self.V.unsqueeze(0)
 
         def op(name):
             if events is None:
@@ -107,15 +142,24 @@ class DecoderLayer:
                                      T, H, [dm.q_cols, dm.kv_cols, dm.kv_cols])))
         Q = self._buf("Q", (dm.Hq, T, D_HEAD))
         with op("kv_append"):
-            rmm.rmm_qkv_heads(yq, yk, yv, Q, self.Kt, self.V, L0)
+            if tree or self.q_norm is not None or self.k_norm is not None or self.inv_freq is not None:
+                rmm.rmm_qkv_rope(yq, yk, yv, Q.unsqueeze(0), Kt, V, lens=lens, L0=0 if tree else L0, parents=parents,
+                                 q_norm=self.q_norm, k_norm=self.k_norm, eps=dm.eps, inv_freq=self.inv_freq,
+                                 interleaved=self.interleaved)
+            else:
+                rmm.rmm_qkv_heads(yq, yk, yv, Q, self.Kt, self.V, L0)
         L = L0 + T
         idx_attn = torch.empty(1, dm.Hkv, rmm.rmm_k_for(D_HEAD, r), dtype=torch.int32, device=self.dev)
         O = self._buf("O", (1, dm.Hq, T, D_HEAD))
         with op("attention"):
-            rmm.rmm_attn_qk(Q.unsqueeze(0), self.Kt.unsqueeze(0), self.V.unsqueeze(0), L, r, causal=True,
-                            O=O, idx_out=idx_attn,
-                            workspace=self._ws_for(("attn", T), rmm.rmm_attn_workspace_bytes(
-                                1, dm.Hq, dm.Hkv, T, self.ldL, D_HEAD)))
+            if tree:
+                rmm.rmm_attn_tree(Q.unsqueeze(0), Kt, V, lens, r, parents=parents, O=O, idx_out=idx_attn,
+                                  workspace=self._ws_for(("attn_tree", T), rmm.rmm_attn_tree_workspace_bytes(
+                                      1, dm.Hq, dm.Hkv, T, self.ldL, D_HEAD)))
+            else:
+                rmm.rmm_attn_qk(Q.unsqueeze(0), Kt, V, L, r, causal=True, O=O, idx_out=idx_attn,
+                                workspace=self._ws_for(("attn", T), rmm.rmm_attn_workspace_bytes(
+                                    1, dm.Hq, dm.Hkv, T, self.ldL, D_HEAD)))
         with op("heads_to_tokens"):
             a = rmm.rmm_heads_to_tokens(O[0], A=self._buf("a", (T, dm.q_cols)))
         idx_o = self._idx("o", dm.q_cols)
@@ -149,7 +193,6 @@ class DecoderLayer:
         out = torch.empty(T, H, dtype=torch.bfloat16, device=self.dev)
         with op("residual"):
             rmm.rmm_add_rmsnorm(h2, yd, eps=dm.eps, Hsum=out, want_y=False)
-        self.pos = L
         if trace is not None:
             # copies: the activation buffers are reused by the next call
             vals = dict(x=x, xn=xn, yq=yq, yk=yk, yv=yv, Q=Q, L0=L0, L=L, O=O[0], a=a, yo=yo, h2=h2, xn2=xn2,
@@ -161,6 +204,66 @@ class DecoderLayer:
 
     def _idx(self, name, H):
         return torch.empty(H, dtype=torch.int32, device=self.dev)
+
+
+class OutputHead:
+    """Hidden rows to next-token probabilities: RMSNorm, the product with the output weights [V, H] at ratio r,
+    softmax at a temperature."""
+
+    def __init__(self, weight: torch.Tensor, r: float, device, eps: float = 1e-5):
+        self.Wt = rmm.rmm_transpose_weight(weight.to(device))
+        self.r = float(r)
+        self.eps = eps
+        self._kept = {}  # row count -> (norm, logits, workspace)
+
+    def probabilities(self, x: torch.Tensor, temperature: float = 1.0) -> torch.Tensor:
+        """x [T, H] bf16 -> fp32 [T, V]; temperature 0 is greedy."""
+        T, (H, V) = x.shape[0], self.Wt.shape
+        if T not in self._kept:
+            self._kept[T] = (torch.empty(T, H, dtype=torch.bfloat16, device=x.device),
+                             torch.empty(T, V, dtype=torch.bfloat16, device=x.device),
+                             rmm.new_workspace(rmm.rmm_linear_workspace_bytes(T, H, V), x.device))
+        xn, logits, ws = self._kept[T]
+        rmm.rmm_add_rmsnorm(x, eps=self.eps, Y=xn)
+        rmm.rmm_linear(xn, self.Wt, self.r, Y=logits, workspace=ws)
+        return rmm.rmm_softmax(logits, temperature)
+
+
+def keep_path(layers, path: torch.Tensor, count: torch.Tensor, lens: torch.Tensor | None = None) -> int:
+    """Keep the nodes path[0, :count[0]] (int32 [1, T], ascending) of the tree that forward_tree scored last, in
+    every layer's cache: their keys and values move up to the cache, pos grows by their number, which is returned
+    (it is read from the device)."""
+    if any(layer.pos != layers[0].pos for layer in layers):
+        raise ValueError("the layers' caches hold different numbers of tokens")
+    if lens is None:
+        lens = torch.full((1,), layers[0].pos, dtype=torch.int32, device=path.device)
+    grown = rmm.rmm_cache_keep([(layer.Kt.unsqueeze(0), layer.V.unsqueeze(0)) for layer in layers], lens, path, count)
+    n = int(grown) - layers[0].pos
+    for layer in layers:
+        layer.pos += n
+    return n
+
+
+def decode_tree(layers, head: OutputHead, embed: torch.Tensor, tokens: torch.Tensor, parents: torch.Tensor,
+                u: torch.Tensor, temperature: float = 1.0, Qd: torch.Tensor | None = None,
+                trace: dict | None = None) -> list[int]:
+    """One step of decoding with drafts.  tokens int32 [T] are the tree's, its root the last token that was emitted
+    (its key is not in the cache yet); parents int32 [T] the tree; embed bf16 [V, H] the tokens' rows; u fp32 [T] in
+    [0, 1), one random number per node, the root's for the next token; Qd fp32 [T, V] the rows that each node's
+    children were drawn from (None: certain picks).  Returns the tokens emitted, one more than the drafts that were
+    accepted: the last of them is the next tree's root.  For any draft they are distributed as sampling one token
+    at a time from the layers would have them, given the kept sets of this pass."""
+    tokens, parents, u = tokens.view(1, -1), parents.view(1, -1), u.view(1, -1)
+    lens = torch.full((1,), layers[0].pos, dtype=torch.int32, device=tokens.device)
+    x = embed.index_select(0, tokens[0].clamp(0, embed.shape[0] - 1))  # other tokens are never accepted
+    for layer in layers:
+        x = layer.forward_tree(x, parents, lens)
+    P = head.probabilities(x, temperature)
+    path, emitted, count = rmm.rmm_tree_verify(P, tokens, parents, u, Qd=Qd)
+    n = keep_path(layers, path, count, lens)
+    if trace is not None:
+        trace.update(x=x, P=P, path=path, emitted=emitted, count=count)
+    return emitted[0, :n].tolist()
 
 
 class DenseLayer:
