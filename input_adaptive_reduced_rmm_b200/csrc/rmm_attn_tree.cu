@@ -15,12 +15,13 @@
 // are stacked, up to 256 to a CTA, and the keys are split.
 //
 // Work: a unit is (sequence, KV head, pair of 128-row tiles); its keys come in
-// blocks of 128.  All units' blocks, in order, are cut into equal shares, one per
+// blocks of 64.  All units, in order, are cut into shares of equal cost, one per
 // CTA (one CTA per SM), wherever the cuts fall: ragged batches balance and few
-// units still fill the GPU.  A unit inside one share is finished there; one that
-// was cut leaves fp32 partials (maximum, sum, unnormalised output), at most two
-// per CTA, which a second kernel joins.  Lengths are read on the device only, so
-// a captured call serves any lengths.
+// units still fill the GPU.  A unit costs its blocks and a constant for its start
+// and end.  A unit inside one share is finished there; one that was cut leaves
+// fp32 partials (maximum, sum, unnormalised output), at most two per CTA, which a
+// second kernel joins.  Lengths are read on the device only, so a captured call
+// serves any lengths.
 //
 // Two softmax groups of four warps (a thread per row) alternate on the tensor
 // cores: with two row tiles each group has its own tile and both use every key
@@ -64,6 +65,10 @@ constexpr int V_CHUNK = BK * 128;  // 64 dims of a value block (bytes)
 constexpr int V_BYTES = 2 * V_CHUNK;
 constexpr uint32_t TM_O = 256;  // S of group a at 128 a (two buffers), O of group a at 256 + 128 a
 constexpr float kRescaleLog2 = 8.0f;
+// Blocks that the start and the end of a unit's piece take the time of, in the share of work that
+// a CTA gets (every dim kept, us for 32 x 8k decode: 113 without, 104 at 3, 103 at 6, 104 at 10;
+// fewer kept, tree of 25 over 8 x 16k: 78 without, 73.5 at 3, 71.5 at 6, 70 at 10).
+__host__ __device__ constexpr int piece_cost(bool all) { return all ? 6 : 10; }
 constexpr int kSmemMax = 232448;  // 227 KB
 
 struct __align__(8) TreeBars {
@@ -73,8 +78,7 @@ struct __align__(8) TreeBars {
     uint64_t s_full[2][2], p_full[2][2];  // [group][buffer]
     uint64_t pv_done[2];
     uint64_t meet;  // all softmax warps
-    long long pos;  // the CTA's share: first block, and how many
-    int seg_b, seg_u, seg_blk, blocks;
+    int seg_b, seg_u, seg_x, cost, piece;  // the CTA's share: where it starts, and how much it is
     uint32_t tmem_base;
     int abort_flag;
 };
@@ -85,7 +89,7 @@ struct TreeArgs {
     int32_t* idx;  // kept sets [B * Hkv * k]
     uint16_t* O;
     float* partials;
-    long long* cum;  // [B + 1]: blocks of the sequences before b
+    long long* cum;  // [B + 1]: cost of the sequences before b; then how many shares, and the cost of a piece
     int* status;
     int B, Hkv, G, T, ldL, R, nrt, nrp, k, kp, nk, nv, slot_rows;
     int identity;    // every dim kept
@@ -97,26 +101,30 @@ __device__ __forceinline__ int blocks_of(const TreeArgs& a, int b) {
     return len < 0 || len > a.ldL - a.T ? 0 : (len + a.T + BK - 1) / BK;
 }
 
-// A CTA's share as its roles walk it, one piece of a unit at a time.
+// A CTA's share as its roles walk it, one piece of a unit at a time.  A unit of nb blocks
+// costs nb + piece: the places [0, piece) stand for the start and end of its pieces, place
+// piece + i for block i.
 struct Share {
-    int b, u, blk, left, n, nb;  // n: blocks of this piece, nb: of the whole unit
+    int b, u, x, left, cost, blk, n, nb;  // blk, n: the piece's first block and how many, nb: of the whole unit
     __device__ __forceinline__ bool next(const TreeArgs& a, const TreeBars* s, bool first) {
         if (first) {
-            b = s->seg_b, u = s->seg_u, blk = s->seg_blk, left = s->blocks;
+            b = s->seg_b, u = s->seg_u, x = s->seg_x, left = s->cost;
             if (left <= 0) return false;
             nb = blocks_of(a, b);
         } else {
-            left -= n;
+            left -= cost;
             if (left <= 0) return false;
-            blk = 0;
+            x = 0;
             if (++u == a.Hkv * a.nrp) {
                 u = 0;
                 do nb = blocks_of(a, ++b);
                 while (nb == 0);  // left > 0: a later sequence has blocks
             }
         }
-        n = min(nb - blk, left);
-        return true;
+        cost = min(nb + s->piece - x, left);
+        blk = max(x - s->piece, 0);
+        n = x + cost - s->piece - blk;
+        return n > 0;  // a share may end before a unit's first block
     }
 };
 
@@ -159,24 +167,60 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     return r;
 }
 
+// The exponentials' instructions in the order written: left to itself the compiler put each
+// sum right behind its exponential, and a warp waited 1100 cycles for 64 of them instead of 610.
+__device__ __forceinline__ float exp2_here(float x) {
+    float y;
+    asm volatile("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ F2 fma2_here(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm volatile("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+__device__ __forceinline__ F2 add2_here(F2 a, F2 b) {
+    F2 r;
+    asm volatile("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+
 // p = 2^(x scale - m) for 64 logits of a row, their sum, and P (bf16) to the 32
-// columns at pcol.
-__device__ __forceinline__ float exp_block(const uint32_t (&x)[2][32], float scale_log2, float neg_m, uint32_t pcol) {
-    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+// columns at pcol; kBatch exponentials are on their way while those before are summed.
+__device__ __forceinline__ float exp_block(uint32_t (&x)[2][32], float scale_log2, float neg_m, uint32_t pcol) {
+    constexpr int kBatch = 16;
+    F2 sum[4] = {F2(0.f, 0.f), F2(0.f, 0.f), F2(0.f, 0.f), F2(0.f, 0.f)};
+    const F2 scale(scale_log2, scale_log2), shift(neg_m, neg_m);
+    uint32_t pk[2][16];
 #pragma unroll
-    for (int q = 0; q < 2; ++q) {
-        uint32_t pk[16];
+    for (int b = 0; b <= 64; b += kBatch) {
 #pragma unroll
-        for (int c = 0; c < 32; c += 2) {
-            const float p0 = fast_exp2(fmaf(__uint_as_float(x[q][c]), scale_log2, neg_m));
-            const float p1 = fast_exp2(fmaf(__uint_as_float(x[q][c + 1]), scale_log2, neg_m));
-            sum[c & 2] += p0;
-            sum[(c & 2) + 1] += p1;
-            pk[c >> 1] = pack2(p0, p1);
+        for (int c = b; c < b + kBatch && b < 64; c += 2) {
+            uint32_t &u0 = x[c >> 5][c & 31], &u1 = x[c >> 5][(c & 31) + 1];
+            float z0, z1;
+            fma2_here(F2(__uint_as_float(u0), __uint_as_float(u1)), scale, shift).get(z0, z1);
+            u0 = __float_as_uint(z0), u1 = __float_as_uint(z1);
         }
-        tmem_st_32x32b_x16(pcol + q * 16, pk);
+#pragma unroll
+        for (int c = b; c < b + kBatch; c += 2) {
+            if (b < 64) {
+                uint32_t &u0 = x[c >> 5][c & 31], &u1 = x[c >> 5][(c & 31) + 1];
+                u0 = __float_as_uint(exp2_here(__uint_as_float(u0)));
+                u1 = __float_as_uint(exp2_here(__uint_as_float(u1)));
+            }
+            if (b > 0) {
+                const int d = c - kBatch;
+                const float p0 = __uint_as_float(x[d >> 5][d & 31]), p1 = __uint_as_float(x[d >> 5][(d & 31) + 1]);
+                sum[(d >> 1) & 3] = add2_here(sum[(d >> 1) & 3], F2(p0, p1));
+                pk[d >> 5][(d & 31) >> 1] = pack2(p0, p1);
+            }
+        }
+        if (b == 32) tmem_st_32x32b_x16(pcol, pk[0]);
+        if (b == 64) tmem_st_32x32b_x16(pcol + 16, pk[1]);
     }
-    return (sum[0] + sum[1]) + (sum[2] + sum[3]);
+    float s0, s1;
+    add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])).get(s0, s1);
+    return s0 + s1;
 }
 
 // umma_f16, umma_f16_tmem_a and umma_commit by one thread of a converged warp (the
@@ -262,24 +306,32 @@ __global__ void __launch_bounds__(tree_threads(kAll), 1)
     pdl_wait();  // lengths, trees, kept sets, queries and caches come from the preceding kernels
     pdl_launch_dependents();
     if (warp == 0) {
-        // the CTA's share of all blocks, and where it starts; the last CTA also leaves the
-        // running counts for the joining kernel
+        // the CTA's share of the whole cost, and where it starts; the last CTA also leaves the
+        // running costs for the joining kernel
         const int U = a.Hkv * a.nrp, c = blockIdx.x;
-        long long total = 0;
+        long long blocks = 0, seqs = 0;
+        const int mine = lane < a.B ? blocks_of(a, lane) : 0;  // of the first 32 sequences
         for (int b = lane; b < a.B; b += 32) {
-            total += blocks_of(a, b);
+            const int nb = b == lane ? mine : blocks_of(a, b);
+            blocks += nb;
+            seqs += nb > 0;
             if (c == 0 && a.lens[b] > a.ldL - a.T) record_status(status, RMM_ERR_INVALID_ARG);
         }
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-        total *= U;
-        // never more shares than blocks: no share between two others is empty
-        const long long C = min((long long)gridDim.x, total);
+        for (int o = 16; o > 0; o >>= 1) {
+            blocks += __shfl_xor_sync(0xffffffffu, blocks, o);
+            seqs += __shfl_xor_sync(0xffffffffu, seqs, o);
+        }
+        // shares of more than piece_cost + 1, and never more of them than blocks: none is empty
+        const long long C = min((long long)gridDim.x, blocks * U);
+        const int piece = blocks * U >= C * (2 * piece_cost(kAll)) ? piece_cost(kAll) : 0;
+        const long long total = (blocks + seqs * piece) * U;
         const long long p0 = c < C ? total * c / C : total, p1 = c < C ? total * (c + 1) / C : total;
         long long base = 0;
         for (int b0 = 0; b0 < a.B; b0 += 32) {
             const int b = b0 + lane;
-            const long long n = b < a.B ? (long long)blocks_of(a, b) * U : 0;
+            const int nb = b0 == 0 ? mine : b < a.B ? blocks_of(a, b) : 0;
+            const long long n = nb ? (long long)(nb + piece) * U : 0;
             long long end = n;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -292,15 +344,18 @@ __global__ void __launch_bounds__(tree_threads(kAll), 1)
                 if (b == 0) a.cum[0] = 0;
             }
             if (p0 < end && p0 >= end - n) {  // one lane of one round
-                const int nb = (int)(n / U);
-                const long long in = p0 - (end - n);
+                const uint32_t in = (uint32_t)(p0 - (end - n));  // below U (ldL / BK + piece_cost) < 2^32
                 bars->seg_b = b;
-                bars->seg_u = (int)(in / nb);
-                bars->seg_blk = (int)(in % nb);
+                bars->seg_u = (int)(in / (uint32_t)(nb + piece));
+                bars->seg_x = (int)(in % (uint32_t)(nb + piece));
             }
             base = __shfl_sync(0xffffffffu, end, 31);
         }
-        if (lane == 0) bars->blocks = (int)(p1 - p0);
+        if (lane == 0) {
+            bars->cost = (int)(p1 - p0);
+            bars->piece = piece;
+            if (c == (int)gridDim.x - 1) a.cum[a.B + 1] = C, a.cum[a.B + 2] = piece;
+        }
     }
     tc_fence_before();
     __syncthreads();
@@ -346,19 +401,54 @@ __global__ void __launch_bounds__(tree_threads(kAll), 1)
                 ++queries;
                 if (w.blk == 0 && rp == 0 && a.idx && tid < D) a.idx[(size_t)plane * D + tid] = tid;
             } else {
-                // the kept dims of 8 rows at a time
-                const int32_t* S = a.idx + (size_t)plane * a.k;
-                for (int it = tid; it < kp * 16 * tiles; it += kSoftmaxThreads) {
-                    const int jr = it % kp, c16 = (it / kp) & 15, t = it / (kp * 16);
-                    const int dim = jr < a.k ? S[jr] : -1;
-                    const int r = (2 * rp + t) * BM + c16 * 8;
-                    uint16_t v[8];
+                // a thread turns 8 rows x 8 dims of each tile and puts the kept dims at their places
+                const int c = tid & 15, c16 = tid >> 4;
+                uint4 v[2][8];
 #pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        v[e] = dim >= 0 && r + e < a.R ? a.Q[(row0 + r + e) * D + dim] : (uint16_t)0;
-                    st_shared_v4(smem_addr(sQ + t * Q_BYTES) + swz(jr, c16, kp * 128),
-                                 make_uint4(v[0] | ((uint32_t)v[1] << 16), v[2] | ((uint32_t)v[3] << 16),
-                                            v[4] | ((uint32_t)v[5] << 16), v[6] | ((uint32_t)v[7] << 16)));
+                for (int t = 0; t < 2; ++t)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const int r = (2 * rp + t) * BM + c16 * 8 + e;
+                        v[t][e] = t < tiles && r < a.R ? *reinterpret_cast<const uint4*>(a.Q + (row0 + r) * D + c * 8)
+                                                       : make_uint4(0, 0, 0, 0);
+                    }
+                const int32_t* S = a.idx + (size_t)plane * a.k;
+                int d[4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) d[q] = lane + 32 * q < a.k ? S[lane + 32 * q] : -1;
+                uint32_t kept = 0;  // the dims of this thread's 32, and how many come before
+                int before = 0;
+#pragma unroll
+                for (int w4 = 0; w4 < 4; ++w4) {
+                    uint32_t m = 0;
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) m |= (d[q] >> 5) == w4 ? 1u << (d[q] & 31) : 0u;
+                    m = __reduce_or_sync(0xffffffffu, m);
+                    if (w4 < (c >> 2)) before += __popc(m);
+                    if (w4 == (c >> 2)) kept = m;
+                }
+                before += __popc(kept & ((1u << ((c & 3) * 8)) - 1u));
+                kept >>= (c & 3) * 8;
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    if (t >= tiles) break;
+                    const uint32_t base = smem_addr(sQ + t * Q_BYTES);
+                    int j = before;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const uint32_t sel = e & 1 ? 0x7632u : 0x5410u;
+                        uint32_t w[8];
+#pragma unroll
+                        for (int r = 0; r < 8; ++r)
+                            w[r] = e < 2 ? v[t][r].x : e < 4 ? v[t][r].y : e < 6 ? v[t][r].z : v[t][r].w;
+                        if ((kept >> e) & 1u) {
+                            st_shared_v4(base + swz(j, c16, kp * 128),
+                                         make_uint4(__byte_perm(w[0], w[1], sel), __byte_perm(w[2], w[3], sel),
+                                                    __byte_perm(w[4], w[5], sel), __byte_perm(w[6], w[7], sel)));
+                            ++j;
+                        }
+                    }
+                    for (j = a.k + c; j < kp; j += 16) st_shared_v4(base + swz(j, c16, kp * 128), make_uint4(0, 0, 0, 0));
                 }
                 fence_proxy_async_smem();
                 mbar_arrive(smem_addr(&bars->q_full));
@@ -468,7 +558,7 @@ __global__ void __launch_bounds__(tree_threads(kAll), 1)
             tc_fence_after();
             if (way == 0) m_use = -INFINITY, l = 0.0f;  // an absent node sees nothing
             const bool whole = w.n == w.nb;
-            float* slot = a.partials + (size_t)(2 * blockIdx.x + (w.left == bars->blocks ? 0 : 1)) * slot_floats(a.slot_rows);
+            float* slot = a.partials + (size_t)(2 * blockIdx.x + (w.left == bars->cost ? 0 : 1)) * slot_floats(a.slot_rows);
             const bool second = w.n > 1;  // with one tile: group 1 had a block, O1 holds this unit's data
             float m0 = 0.f, m1 = 0.f, l0 = 0.f, l1 = 0.f;
             if (!two) {  // both groups hold a part of the same rows
@@ -736,18 +826,18 @@ __global__ void __launch_bounds__(tree_threads(kAll), 1)
 // partials' bytes.
 constexpr int kJoinRows = 8;
 
-__global__ void __launch_bounds__(kJoinRows * 32) attn_tree_join_kernel(const TreeArgs a, int ctas) {
+__global__ void __launch_bounds__(kJoinRows * 32) attn_tree_join_kernel(const TreeArgs a) {
     const int U = a.Hkv * a.nrp, tid = threadIdx.x;
     const int unit = blockIdx.x, b = unit / U, u = unit % U, g = u / a.nrp, rp = u % a.nrp;
     const int r = blockIdx.y * kJoinRows + (tid & (kJoinRows - 1)), c4 = tid / kJoinRows;
     if (r >= min(2 * BM, a.R - rp * 2 * BM)) return;
     pdl_wait();
     pdl_launch_dependents();
-    const long long lo = a.cum[b], hi = a.cum[b + 1], total = a.cum[a.B];
-    const long long nb = (hi - lo) / U, C = min((long long)ctas, total);
-    const long long p0 = lo + u * nb, p1 = p0 + nb;  // the unit's blocks
-    // share c is [total c / C, total (c + 1) / C): the shares of its first and last block
-    const int c0 = nb ? (int)(((p0 + 1) * C - 1) / total) : 0, c1 = nb ? (int)((p1 * C - 1) / total) : 0;
+    const long long lo = a.cum[b], hi = a.cum[b + 1], total = a.cum[a.B], C = a.cum[a.B + 1], piece = a.cum[a.B + 2];
+    const long long cost = (hi - lo) / U, nb = cost ? cost - piece : 0;
+    const long long p0 = lo + u * cost;  // where the unit starts, its blocks `piece` later
+    // share c is [total c / C, total (c + 1) / C): the shares of the unit's first and last block
+    const int c0 = nb ? (int)(((p0 + piece + 1) * C - 1) / total) : 0, c1 = nb ? (int)(((p0 + cost) * C - 1) / total) : 0;
     if (nb && c0 == c1) return;
     const int n = nb ? c1 - c0 + 1 : 0;
     const size_t sf = slot_floats(a.slot_rows);
@@ -878,7 +968,7 @@ TreePlan tree_plan(int B, int Hq, int Hkv, int T, int ldL, int num_sms) {
     return p;
 }
 
-size_t cum_bytes(int B) { return ((size_t)(B + 1) * sizeof(long long) + 255) / 256 * 256; }
+size_t cum_bytes(int B) { return ((size_t)(B + 3) * sizeof(long long) + 255) / 256 * 256; }
 
 }  // namespace
 
@@ -929,7 +1019,7 @@ cudaError_t launch_attn_tree(const CUtensorMap& qmap, const CUtensorMap& kmap, c
     if (e != cudaSuccess) return e;
     const int most_rows = p.R < 2 * BM ? p.R : 2 * BM;
     return launch_pdl(attn_tree_join_kernel, dim3(B * Hkv * p.nrp, (most_rows + kJoinRows - 1) / kJoinRows),
-                      dim3(kJoinRows * 32), 0, stream, a, p.ctas);
+                      dim3(kJoinRows * 32), 0, stream, a);
 }
 
 }  // namespace rmm
