@@ -66,8 +66,8 @@ constexpr int V_BYTES = 2 * V_CHUNK;
 constexpr uint32_t TM_O = 256;  // S of group a at 128 a (two buffers), O of group a at 256 + 128 a
 constexpr float kRescaleLog2 = 8.0f;
 // Blocks that the start and the end of a unit's piece take the time of, in the share of work that
-// a CTA gets (every dim kept, us for 32 x 8k decode: 113 without, 104 at 3, 103 at 6, 104 at 10;
-// fewer kept, tree of 25 over 8 x 16k: 78 without, 73.5 at 3, 71.5 at 6, 70 at 10).
+// a CTA gets (every dim kept, us for 32 x 8k decode: 112 without, 104 at 3, 103 at 6, 104 at 10;
+// fewer kept, tree of 25 over 8 x 16k: 79 without, 73.5 at 3, 71.5 at 6, 70 at 10).
 __host__ __device__ constexpr int piece_cost(bool all) { return all ? 6 : 10; }
 constexpr int kSmemMax = 232448;  // 227 KB
 
@@ -97,7 +97,7 @@ struct TreeArgs {
 };
 
 __device__ __forceinline__ int blocks_of(const TreeArgs& a, int b) {
-    const int len = a.lens[b];
+    const int len = __ldcg(a.lens + b);
     return len < 0 || len > a.ldL - a.T ? 0 : (len + a.T + BK - 1) / BK;
 }
 
@@ -303,7 +303,10 @@ __global__ void __launch_bounds__(tree_threads(kAll), 1)
         tma_prefetch_desc(&vmap);
         tma_prefetch_desc(&qmap);
     }
-    pdl_wait();  // lengths, trees, kept sets, queries and caches come from the preceding kernels
+    // Lengths, trees, queries and caches come from kernels before this call.  Where the kept sets'
+    // kernel goes first, it has waited for those before it let this one start, and only what reads
+    // the sets waits for it; reads before that go past the L1 cache.
+    if (kAll) pdl_wait();
     pdl_launch_dependents();
     if (warp == 0) {
         // the CTA's share of the whole cost, and where it starts; the last CTA also leaves the
@@ -315,7 +318,7 @@ __global__ void __launch_bounds__(tree_threads(kAll), 1)
             const int nb = b == lane ? mine : blocks_of(a, b);
             blocks += nb;
             seqs += nb > 0;
-            if (c == 0 && a.lens[b] > a.ldL - a.T) record_status(status, RMM_ERR_INVALID_ARG);
+            if (c == 0 && __ldcg(a.lens + b) > a.ldL - a.T) record_status(status, RMM_ERR_INVALID_ARG);
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) {
@@ -388,7 +391,7 @@ __global__ void __launch_bounds__(tree_threads(kAll), 1)
             const int rp = w.u % a.nrp, plane = w.b * a.Hkv + w.u / a.nrp;
             const int tiles = 2 * rp + 1 < a.nrt ? 2 : 1;
             const size_t row0 = (size_t)plane * a.R;
-            if (a.parents && tid < a.T) par[tid] = a.parents[(size_t)w.b * a.T + tid];
+            if (a.parents && tid < a.T) par[tid] = __ldcg(a.parents + (size_t)w.b * a.T + tid);
             if (kAll) {
                 if (tid == 0) {
                     const uint32_t qf = smem_addr(&bars->q_full), qb = smem_addr(sQ);
@@ -409,9 +412,10 @@ __global__ void __launch_bounds__(tree_threads(kAll), 1)
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
                         const int r = (2 * rp + t) * BM + c16 * 8 + e;
-                        v[t][e] = t < tiles && r < a.R ? *reinterpret_cast<const uint4*>(a.Q + (row0 + r) * D + c * 8)
+                        v[t][e] = t < tiles && r < a.R ? __ldcg(reinterpret_cast<const uint4*>(a.Q + (row0 + r) * D + c * 8))
                                                        : make_uint4(0, 0, 0, 0);
                     }
+                pdl_wait();  // the kept sets
                 const int32_t* S = a.idx + (size_t)plane * a.k;
                 int d[4];
 #pragma unroll
@@ -461,7 +465,7 @@ __global__ void __launch_bounds__(tree_threads(kAll), 1)
             const int g = w.u / a.nrp, rp = w.u % a.nrp;
             const bool two = 2 * rp + 1 < a.nrt;
             const int plane = w.b * a.Hkv + g;
-            const int len = a.lens[w.b];
+            const int len = __ldcg(a.lens + w.b);
             const int tile = 2 * rp + (two ? grp : 0);
             const int row = tile * BM + i;  // of the unit's G * T rows: query head row / T, node row % T
             const size_t row0 = (size_t)plane * a.R;
@@ -784,6 +788,7 @@ __global__ void __launch_bounds__(tree_threads(kAll), 1)
         // instruction takes about 110 cycles to leave, so that two warps of them bounded the
         // kernel (1750 cycles a block at 64 kept dims, where its bytes take 1000).
         const int c16 = lane & 7, row = (warp - kGatherWarp) * 4 + (lane >> 3);
+        pdl_wait();
         Ring k;
         bool ok = true;
         for (bool more = w.next(a, bars, true); ok && more; more = w.next(a, bars, false)) {
@@ -814,23 +819,25 @@ __global__ void __launch_bounds__(tree_threads(kAll), 1)
         cp_async_wait_all();  // no copy may still be landing when the CTA leaves
     }
 
+    if (!kAll) pdl_wait();  // nothing is left of the kept sets' kernel when this one ends
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
 }
 
-// The partials of a unit that was cut, joined; also the zeros of empty slots.  A
-// thread takes four dims of a row, eight pieces in flight, with a running maximum.
-// Bound by the latency of two dependent reads from L2 and, with many rows, by the
-// partials' bytes.
-constexpr int kJoinRows = 8;
+// The partials of a unit that was cut, joined; also the zeros of empty slots.
+// kLanes threads take four dims of a row, each every kLanes-th piece with four of
+// them in flight and a running maximum.  Bound by the latency of two dependent reads
+// from L2 and, with many rows, by the partials' bytes.
+constexpr int kJoinThreads = 256;
 
-__global__ void __launch_bounds__(kJoinRows * 32) attn_tree_join_kernel(const TreeArgs a) {
-    const int U = a.Hkv * a.nrp, tid = threadIdx.x;
+template <int kLanes>
+__global__ void __launch_bounds__(kJoinThreads) attn_tree_join_kernel(const TreeArgs a) {
+    constexpr int kRows = kJoinThreads / 32 / kLanes, kFly = 4;
+    const int U = a.Hkv * a.nrp, z = threadIdx.x % kLanes, tid = threadIdx.x / kLanes;
     const int unit = blockIdx.x, b = unit / U, u = unit % U, g = u / a.nrp, rp = u % a.nrp;
-    const int r = blockIdx.y * kJoinRows + (tid & (kJoinRows - 1)), c4 = tid / kJoinRows;
-    if (r >= min(2 * BM, a.R - rp * 2 * BM)) return;
+    const int r = blockIdx.y * kRows + tid % kRows, c4 = tid / kRows;
     pdl_wait();
     pdl_launch_dependents();
     const long long lo = a.cum[b], hi = a.cum[b + 1], total = a.cum[a.B], C = a.cum[a.B + 1], piece = a.cum[a.B + 2];
@@ -840,23 +847,27 @@ __global__ void __launch_bounds__(kJoinRows * 32) attn_tree_join_kernel(const Tr
     const int c0 = nb ? (int)(((p0 + piece + 1) * C - 1) / total) : 0, c1 = nb ? (int)(((p0 + cost) * C - 1) / total) : 0;
     if (nb && c0 == c1) return;
     const int n = nb ? c1 - c0 + 1 : 0;
+    const int rows = min(2 * BM, a.R - rp * 2 * BM), row = min(r, rows - 1);
     const size_t sf = slot_floats(a.slot_rows);
     // the first share may have begun with another unit: its piece is then its second
     const int skip = nb && total * c0 / C < p0 ? 1 : 0;
     const float* base = a.partials + (size_t)(2 * c0) * sf;
-    const size_t at = ((size_t)c4 * a.slot_rows + r) * 4;
+    const size_t at = ((size_t)c4 * a.slot_rows + row) * 4;
     float M = -INFINITY, L = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    constexpr int kFly = 8;
-    for (int i0 = 0; i0 < n; i0 += kFly) {
+    for (int i0 = z; i0 < n; i0 += kFly * kLanes) {
         float m[kFly], l[kFly];
         float4 v[kFly];
 #pragma unroll
         for (int i = 0; i < kFly; ++i) {
-            const float* p = base + (size_t)(2 * min(i0 + i, n - 1) + (i0 + i == 0 ? skip : 0)) * sf;
-            m[i] = i0 + i < n ? p[D * a.slot_rows + r] : -INFINITY;
-            l[i] = p[(D + 1) * a.slot_rows + r];
-            v[i] = *reinterpret_cast<const float4*>(p + at);
+            const int j = i0 + i * kLanes;
+            m[i] = -INFINITY;
+            if (j < n) {
+                const float* p = base + (size_t)(2 * j + (j == 0 ? skip : 0)) * sf;
+                m[i] = p[D * a.slot_rows + row];
+                l[i] = p[(D + 1) * a.slot_rows + row];
+                v[i] = *reinterpret_cast<const float4*>(p + at);
+            }
         }
         float top = M;
 #pragma unroll
@@ -878,6 +889,20 @@ __global__ void __launch_bounds__(kJoinRows * 32) attn_tree_join_kernel(const Tr
             }
         }
     }
+#pragma unroll
+    for (int d = 1; d < kLanes; d *= 2) {
+        const float top = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
+        const float w = M > -INFINITY ? exp2f(M - top) : 0.f;
+        M = top;
+        L *= w;
+        o.x *= w, o.y *= w, o.z *= w, o.w *= w;
+        L += __shfl_xor_sync(0xffffffffu, L, d);
+        o.x += __shfl_xor_sync(0xffffffffu, o.x, d);
+        o.y += __shfl_xor_sync(0xffffffffu, o.y, d);
+        o.z += __shfl_xor_sync(0xffffffffu, o.z, d);
+        o.w += __shfl_xor_sync(0xffffffffu, o.w, d);
+    }
+    if (z > 0 || r >= rows) return;
     const float inv = L > 0.f ? 1.0f / L : 0.f;
     *reinterpret_cast<uint2*>(a.O + (((size_t)b * a.Hkv + g) * a.R + rp * 2 * BM + r) * D + c4 * 4) =
         make_uint2(pack2(o.x * inv, o.y * inv), pack2(o.z * inv, o.w * inv));
@@ -1017,9 +1042,13 @@ cudaError_t launch_attn_tree(const CUtensorMap& qmap, const CUtensorMap& kmap, c
     }
     e = launch_pdl(kern, dim3(p.ctas), dim3(tree_threads(a.identity)), smem, stream, qmap, kmap, vmap, a);
     if (e != cudaSuccess) return e;
+    // With few units a unit is cut into many pieces, which four threads then share (us of a call, one
+    // thread against four: 16 nodes of one sequence, 18 pieces a unit, 22.3 and 21.2; 25 nodes of 8
+    // sequences, 2 or 3 pieces, 65 and 74).
+    const int units = B * Hkv * p.nrp, lanes = p.ctas > 4 * units ? 4 : 1, rows = kJoinThreads / 32 / lanes;
     const int most_rows = p.R < 2 * BM ? p.R : 2 * BM;
-    return launch_pdl(attn_tree_join_kernel, dim3(B * Hkv * p.nrp, (most_rows + kJoinRows - 1) / kJoinRows),
-                      dim3(kJoinRows * 32), 0, stream, a);
+    return launch_pdl(lanes == 4 ? attn_tree_join_kernel<4> : attn_tree_join_kernel<1>,
+                      dim3(units, (most_rows + rows - 1) / rows), dim3(kJoinThreads), 0, stream, a);
 }
 
 }  // namespace rmm
