@@ -7,6 +7,7 @@ there is no fallback path, and a missing library raises on first use.
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import math
 import os
@@ -141,12 +142,12 @@ def _ptr(t):
 _current_handle = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _stream(stream):
+def _stream(stream, device=None):
     if stream is not None:
         return stream.cuda_stream
     if _current_handle is None:
         return torch.cuda.current_stream().cuda_stream
-    return _current_handle(torch.cuda.current_device())
+    return _current_handle(torch.cuda.current_device() if device is None else device)
 
 
 def _opt(o):
@@ -544,21 +545,24 @@ def rmm_selftest_exp2_fma(x: torch.Tensor, y: torch.Tensor | None = None, stream
 TREE_MAX = 64  # nodes per tree
 
 
-def _here(**tensors):
-    """Every tensor on the current CUDA device: the kernels are launched there."""
+def _here(names, *tensors):
+    """Every tensor on the current CUDA device, where the kernels are launched: its index.  names (one string)
+    for the message."""
     dev = None
-    for name, t in tensors.items():
+    for i, t in enumerate(tensors):
         if t is None:
             continue
         d = t.get_device()
         if d == dev:
             continue
+        name = names.split()[i]
         if not t.is_cuda:
             raise ValueError(f"{name} must be a CUDA tensor")
         if dev is None:
             dev = torch.cuda.current_device()
         if d != dev:
             raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
+    return dev
 
 
 def _new(shape, dtype, like, stream):
@@ -604,11 +608,11 @@ def rmm_qkv_rope(Yq: torch.Tensor, Yk: torch.Tensor, Yv: torch.Tensor, Q: torch.
         _dims(inv_freq, "inv_freq", 1)
         _need(inv_freq, "inv_freq", torch.float32)
         rot = 2 * inv_freq.numel()
-    _here(Yq=Yq, Yk=Yk, Yv=Yv, Q=Q, Kt=Kt, V=V, lens=lens, parents=parents, q_norm=q_norm, k_norm=k_norm,
-          inv_freq=inv_freq)
+    dev = _here("Yq Yk Yv Q Kt V lens parents q_norm k_norm inv_freq", Yq, Yk, Yv, Q, Kt, V, lens, parents, q_norm,
+                k_norm, inv_freq)
     _check(lib().rmm_qkv_rope(_ptr(Yq), _ptr(Yk), _ptr(Yv), B, T, Hq, Hkv, d, _ptr(q_norm), _ptr(k_norm), float(eps),
                               _ptr(inv_freq), rot, int(bool(interleaved)), _ptr(lens), int(L0), _ptr(parents),
-                              _ptr(Q), _ptr(Kt), _ptr(V), ldL, _stream(stream)), "rmm_qkv_rope")
+                              _ptr(Q), _ptr(Kt), _ptr(V), ldL, _stream(stream, dev)), "rmm_qkv_rope")
     return Q
 
 
@@ -636,7 +640,7 @@ def rmm_attn_tree(Q: torch.Tensor, Kt: torch.Tensor, V: torch.Tensor, lens: torc
     _need(O, "O", shape=(B, Hq, T, d))
     if idx_out is not None:
         _need(idx_out, "idx_out", torch.int32, min_numel=B * Hkv * max(0, rmm_k_for(d, r)))
-    _here(Q=Q, Kt=Kt, V=V, lens=lens, parents=parents, O=O, idx_out=idx_out, workspace=workspace)
+    dev = _here("Q Kt V lens parents O idx_out workspace", Q, Kt, V, lens, parents, O, idx_out, workspace)
     if scale is None:
         scale = 1.0 / math.sqrt(d)
     if O is None:
@@ -647,12 +651,15 @@ def rmm_attn_tree(Q: torch.Tensor, Kt: torch.Tensor, V: torch.Tensor, lens: torc
         rmm_workspace_init(workspace, stream)
     _check(lib().rmm_attn_tree(_ptr(Q), _ptr(Kt), _ptr(V), _ptr(lens), _ptr(parents), B, Hq, Hkv, T, ldL, d, float(r),
                                float(scale), _ptr(O), _ptr(idx_out), _ptr(workspace), workspace.numel(),
-                               _stream(stream), _opt(opts)), "rmm_attn_tree")
+                               _stream(stream, dev), _opt(opts)), "rmm_attn_tree")
     return O
 
 
 def _rows(t, name, dtype, rows=None, V=None):
     """A 2-D tensor whose rows are contiguous (their stride may be larger than V): its row stride."""
+    shape = t.shape
+    if t.dtype is dtype and len(shape) == 2 and t.is_contiguous() and (rows is None or shape == (rows, V)):
+        return shape[1]
     if t.dtype != dtype or t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
         raise ValueError(f"{name} must be a 2-D {dtype} tensor with contiguous rows")
     if rows is not None and t.shape != (rows, V):
@@ -678,10 +685,10 @@ def rmm_softmax(X: torch.Tensor, temperature: float = 1.0, Y: torch.Tensor | Non
     ldx = _rows(X, "X", torch.bfloat16)
     rows, V = X.shape
     ldy = _rows(Y, "Y", torch.float32, rows, V) if Y is not None else V
-    _here(X=X, Y=Y)
+    dev = _here("X Y", X, Y)
     if Y is None:
         Y = _new((rows, V), torch.float32, X, stream)
-    _check(lib().rmm_softmax(_ptr(X), rows, V, ldx, float(temperature), _ptr(Y), ldy, _stream(stream)), "rmm_softmax")
+    _check(lib().rmm_softmax(_ptr(X), rows, V, ldx, float(temperature), _ptr(Y), ldy, _stream(stream, dev)), "rmm_softmax")
     return Y
 
 
@@ -703,7 +710,7 @@ def rmm_tree_verify(P: torch.Tensor, tokens: torch.Tensor, parents: torch.Tensor
     _need(path, "path", torch.int32, shape=(B, T))
     _need(emitted, "emitted", torch.int32, shape=(B, T))
     _need(count, "count", torch.int32, shape=(B,))
-    _here(P=P, tokens=tokens, parents=parents, u=u, Qd=Qd, path=path, emitted=emitted, count=count)
+    dev = _here("P tokens parents u Qd path emitted count", P, tokens, parents, u, Qd, path, emitted, count)
     if path is None:
         path = _new((B, T), torch.int32, tokens, stream)
     if emitted is None:
@@ -711,7 +718,7 @@ def rmm_tree_verify(P: torch.Tensor, tokens: torch.Tensor, parents: torch.Tensor
     if count is None:
         count = _new((B,), torch.int32, tokens, stream)
     _check(lib().rmm_tree_verify(_ptr(P), ldp, _ptr(Qd), ldq, B, T, V, _ptr(tokens), _ptr(parents), _ptr(u),
-                                 _ptr(path), _ptr(emitted), _ptr(count), _stream(stream)), "rmm_tree_verify")
+                                 _ptr(path), _ptr(emitted), _ptr(count), _stream(stream, dev)), "rmm_tree_verify")
     return path, emitted, count
 
 
@@ -725,25 +732,28 @@ def rmm_cache_keep(caches, lens: torch.Tensor, path: torch.Tensor, count: torch.
         raise ValueError("no cache given")
     B, Hkv, d, ldL = _caches(*caches[0])
     bf16, k_shape, v_shape, device = torch.bfloat16, (B, Hkv, d, ldL), (B, Hkv, ldL, d), path.get_device()
+    n = len(caches)
+    kts, vs = [], []
     for Kt, V in caches:
         if not (Kt.dtype is bf16 and V.dtype is bf16 and Kt.shape == k_shape and V.shape == v_shape
                 and Kt.is_contiguous() and V.is_contiguous()
                 and Kt.get_device() == device and V.get_device() == device):
             _need(Kt, "Kt", shape=k_shape)
             _need(V, "V", shape=v_shape)
-            _here(Kt=Kt, V=V, path=path)
+            _here("Kt V path", Kt, V, path)
+        kts.append(Kt.data_ptr())
+        vs.append(V.data_ptr())
     _dims(path, "path", 2)
     T = path.shape[1]
     _need(path, "path", torch.int32, shape=(B, T))
     _need(lens, "lens", torch.int32, shape=(B,))
     _need(count, "count", torch.int32, shape=(B,))
     _need(lens_out, "lens_out", torch.int32, shape=(B,))
-    _here(path=path, lens=lens, count=count, lens_out=lens_out)  # and with path the caches
+    dev = _here("path lens count lens_out", path, lens, count, lens_out)  # and with path the caches
     if lens_out is None:
         lens_out = _new((B,), torch.int32, lens, stream)
-    n = len(caches)
-    kt = (ctypes.c_void_p * n)(*[Kt.data_ptr() for Kt, _ in caches])
-    v = (ctypes.c_void_p * n)(*[V.data_ptr() for _, V in caches])
-    _check(lib().rmm_cache_keep(n, kt, v, B, Hkv, d, ldL, _ptr(lens), _ptr(path), _ptr(count), T, _ptr(lens_out),
-                                _stream(stream)), "rmm_cache_keep")
+    both = array.array("Q", kts + vs)  # the pointers, read during the call
+    base = both.buffer_info()[0]
+    _check(lib().rmm_cache_keep(n, base, base + 8 * n, B, Hkv, d, ldL, _ptr(lens), _ptr(path), _ptr(count), T,
+                                _ptr(lens_out), _stream(stream, dev)), "rmm_cache_keep")
     return lens_out
