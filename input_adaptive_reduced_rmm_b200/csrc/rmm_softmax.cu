@@ -48,8 +48,12 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
-// Merge (m, s): the maximum of two parts, the sum relative to it.  Parts without
-// a finite or infinite element have m = -inf and s = 0.
+// what the logits are taken relative to; nothing but -inf (or NaN) has no maximum
+__device__ __forceinline__ float reference(float m) { return m == -INFINITY ? 0.0f : m; }
+
+// Merge (m, s): the maximum of two parts, the sum relative to it.  Parts of nothing
+// but -inf have m = -inf and s = 0; NaN, which no maximum shows, and +inf, which is no
+// reference, make s NaN.
 __device__ __forceinline__ void merge(float& m, float& s, float m2, float s2, float c) {
     const float mm = fmaxf(m, m2);
     const float a = m == mm ? s : s * ex2((m - mm) * c);
@@ -144,12 +148,11 @@ __global__ void __launch_bounds__(kThreads)
     }
 
     float s = 0.f;
-    if (m > -INFINITY) {
+    const float ref = reference(m);
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
+    for (int i = 0; i < NV; ++i)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) s += ex2((at(i, e) - m) * c);
-    }
+        for (int e = 0; e < 8; ++e) s += ex2((at(i, e) - ref) * c);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     if (lane == 0) red_s[warp] = s;
@@ -166,7 +169,7 @@ __global__ void __launch_bounds__(kThreads)
                   ld_shared_cluster_f32(mapa_shared(smem_addr(&part[1]), j)), c);
         cluster_sync();  // no CTA leaves while another still reads its pair
     }
-    const float inv = 1.0f / s;
+    const float inv = s == 0.0f ? 0.0f : 1.0f / s, ref_row = reference(m);
     float* y = Y + row * ldy;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -174,7 +177,7 @@ __global__ void __launch_bounds__(kThreads)
         if (e0 >= V) continue;
         float p[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) p[e] = m > -INFINITY ? ex2((at(i, e) - m) * c) * inv : 0.0f;
+        for (int e = 0; e < 8; ++e) p[e] = ex2((at(i, e) - ref_row) * c) * inv;
         if (wide_y && e0 + 8 <= V) {
             *reinterpret_cast<float4*>(y + e0) = make_float4(p[0], p[1], p[2], p[3]);
             *reinterpret_cast<float4*>(y + e0 + 4) = make_float4(p[4], p[5], p[6], p[7]);
@@ -229,16 +232,15 @@ __global__ void __launch_bounds__(kRowThreads, kRowCtas)
             s *= ex2((m - mm) * c);
             m = mm;
         }
-        if (m > -INFINITY) {
+        const float ref = reference(m);
 #pragma unroll
-            for (int i = 0; i < kFly; ++i)
+        for (int i = 0; i < kFly; ++i)
 #pragma unroll
-                for (int e = 0; e < 8; ++e) s += ex2((at(r[i], e) - m) * c);
-        }
+            for (int e = 0; e < 8; ++e) s += ex2((at(r[i], e) - ref) * c);
     }
     if (tail) {
-        const uint32_t v = x[vecs * 8 + tid];
-        merge(m, s, __uint_as_float(v << 16), v == 0xFF80u ? 0.f : 1.f, c);
+        const float v = __uint_as_float((uint32_t)x[vecs * 8 + tid] << 16);
+        merge(m, s, fmaxf(v, -INFINITY), ex2((v - reference(v)) * c), c);
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
@@ -260,8 +262,7 @@ __global__ void __launch_bounds__(kRowThreads, kRowCtas)
     for (int j = 0; j < kParts; ++j)
         merge(m, s, ld_shared_cluster_f32(mapa_shared(smem_addr(&part[0]), j)),
               ld_shared_cluster_f32(mapa_shared(smem_addr(&part[1]), j)), c);
-    const float inv = 1.0f / s;
-    const bool any = m > -INFINITY;
+    const float inv = s == 0.0f ? 0.0f : 1.0f / s, ref = reference(m);
     for (int i0 = lo + tid; i0 < hi; i0 += kFly * kRowThreads) {
         uint4 r[kFly];
 #pragma unroll
@@ -272,7 +273,7 @@ __global__ void __launch_bounds__(kRowThreads, kRowCtas)
             if (i0 + i * kRowThreads >= hi) break;
             float p[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) p[e] = any ? ex2((at(r[i], e) - m) * c) * inv : 0.0f;
+            for (int e = 0; e < 8; ++e) p[e] = ex2((at(r[i], e) - ref) * c) * inv;
             float4* d = reinterpret_cast<float4*>(y + (int64_t)(i0 + i * kRowThreads) * 8);
             __stcs(d, make_float4(p[0], p[1], p[2], p[3]));
             __stcs(d + 1, make_float4(p[4], p[5], p[6], p[7]));
@@ -280,7 +281,7 @@ __global__ void __launch_bounds__(kRowThreads, kRowCtas)
     }
     if (tail) {
         const float v = __uint_as_float((uint32_t)x[vecs * 8 + tid] << 16);
-        y[vecs * 8 + tid] = any ? ex2((v - m) * c) * inv : 0.0f;
+        y[vecs * 8 + tid] = ex2((v - ref) * c) * inv;
     }
     cluster_sync();  // no CTA leaves while another still reads its pair
 }

@@ -324,6 +324,28 @@ def test_softmax_greedy_and_empty_rows(rmm, V):
             within(Y[3], torch.full((V,), 1.0 / V, dtype=torch.float64), 96 * H32 / V, "equal logits")
 
 
+@pytest.mark.parametrize("rows,V,ldx", [(5, 10, 16), (3, 4096, 4096), (2, 40000, 40000), (33, 16389, 16392),
+                                        (33, 20480, 20480)])
+def test_softmax_nan_and_infinity_reach_the_whole_row(rmm, rows, V, ldx):
+    """Wherever they stand, and with nothing but -inf beside them."""
+    X = torch.full((rows, ldx), float("nan"), dtype=torch.bfloat16)
+    X[:, :V] = normal(V, rows, V)
+    bad = {0: (float("nan"), V - 1), 1: (float("inf"), V - 1), 2: (float("inf"), 3)}
+    for r, (v, i) in bad.items():
+        if r < rows:
+            X[r, i] = v
+    hidden = [r for r in (3, 4) if r < rows]
+    for r in hidden:  # -inf everywhere else
+        X[r, :V] = -float("inf")
+        X[r, 0 if r == 3 else V - 1] = float("nan")
+    Y = torch.zeros(rows, ldx, device="cuda")
+    y = rmm.rmm_softmax(X.cuda()[:, :V], 0.7, Y=Y[:, :V]).cpu()
+    assert not bool(Y[:, V:].any())
+    for r in range(rows):
+        assert bool(torch.isnan(y[r]).all()) == (r in bad or r in hidden), r
+        assert not bool(torch.isnan(y[r]).any()) or r in bad or r in hidden, r
+
+
 # ---------------------------------------------------------------- verification
 
 def verify_inputs(B, T, V, seed, draft=True, fan=4, noise=1.0, padded=True, roots=True):
