@@ -1,4 +1,5 @@
-"""Build librmm.so in-tree: nvcc for sm_100a, one object per .cu, then a shared link.
+"""Build librmm.so in-tree: nvcc for sm_100a, one object per .cu, then a shared link;
+and _binding.so, the Python module in front of some of its calls (g++, against torch).
 
     python -m input_adaptive_reduced_rmm_b200.build [--force] [--verbose-ptxas]
 
@@ -14,6 +15,7 @@ import glob
 import os
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -21,6 +23,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OBJ = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "librmm.so")
+BINDING_SRC = os.path.join(CSRC, "binding.cpp")
+BINDING = os.path.join(PKG, "_binding.so")
 
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -52,12 +56,39 @@ def _compile(src, verbose_ptxas):
     return obj, p.stderr
 
 
+def _build_binding(force):
+    """Compile csrc/binding.cpp into _binding.so, which finds librmm.so beside itself."""
+    if not force and not _stale(BINDING, [BINDING_SRC, os.path.join(INCLUDE, "rmm.h")]):
+        return
+    import torch
+    from torch.utils import cpp_extension
+
+    inc = cpp_extension.include_paths() + [INCLUDE, sysconfig.get_paths()["include"],
+                                           os.path.join(os.path.dirname(os.path.dirname(NVCC)), "include")]
+    libs = [os.path.join(os.path.dirname(torch.__file__), "lib")]
+    tmp = BINDING + f".tmp{os.getpid()}"
+    cmd = (["g++", "-O2", "-std=c++17", "-shared", "-fPIC", BINDING_SRC, "-o", tmp] + [f"-I{i}" for i in inc] +
+           [f"-L{p}" for p in libs] + [f"-L{PKG}", "-l:librmm.so", "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10",
+                                       "-lc10_cuda", "-Wl,-rpath,$ORIGIN"])
+    p = subprocess.run(cmd, capture_output=True, text=True)
+    if p.returncode != 0:
+        raise RuntimeError(f"g++ failed for {BINDING_SRC}:\n{p.stdout}\n{p.stderr}")
+    os.replace(tmp, BINDING)
+
+
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:
-    """Compile every csrc/*.cu for sm_100a and link librmm.so; returns its path."""
+    """Compile every csrc/*.cu for sm_100a and link librmm.so, then the Python module;
+    returns the library's path."""
+    _build_library(force, verbose_ptxas)
+    _build_binding(force)
+    return LIB
+
+
+def _build_library(force, verbose_ptxas):
     os.makedirs(OBJ, exist_ok=True)
     srcs = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
     if not force and not verbose_ptxas and not _stale(LIB, _deps()):
-        return LIB
+        return
     if force:
         for o in glob.glob(os.path.join(OBJ, "*.o")):
             os.remove(o)
@@ -74,7 +105,6 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
     if p.returncode != 0:
         raise RuntimeError(f"link failed:\n{p.stdout}\n{p.stderr}")
     os.replace(tmp, LIB)
-    return LIB
 
 
 if __name__ == "__main__":

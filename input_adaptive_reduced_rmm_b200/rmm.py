@@ -1,4 +1,5 @@
-"""Thin ctypes binding of librmm (C ABI in include/rmm.h), with the same names.
+"""Thin binding of librmm (C ABI in include/rmm.h), with the same names: ctypes, and for
+the calls of a decoding step a compiled module in front (csrc/binding.cpp).
 
 Argument marshalling only: tensors become device pointers and sizes, the
 current torch stream becomes the cudaStream_t, a non-OK status becomes an
@@ -7,7 +8,6 @@ there is no fallback path, and a missing library raises on first use.
 """
 from __future__ import annotations
 
-import array
 import ctypes
 import math
 import os
@@ -152,6 +152,24 @@ def _stream(stream, device=None):
 
 def _opt(o):
     return None if o is None else ctypes.byref(o)
+
+
+_binding = None
+
+
+def _short():
+    """The compiled module: its functions make the call where everything is as they expect and return its status,
+    else None."""
+    global _binding
+    if _binding is None:
+        lib()
+        try:
+            from . import _binding as module
+        except ImportError as e:
+            raise RuntimeError("the compiled module in front of librmm is missing: build it with "
+                               "`python -m input_adaptive_reduced_rmm_b200.build`") from e
+        _binding = module
+    return _binding
 
 
 def _check(rc: int, what: str):
@@ -590,6 +608,11 @@ def rmm_qkv_rope(Yq: torch.Tensor, Yk: torch.Tensor, Yv: torch.Tensor, Q: torch.
     per-head RMS norms (q_norm, k_norm bf16 [d]) and the rotation by position (inv_freq fp32 [rot/2]).  Sequence
     b is appended at lens[b] (int32 [B]), or all of them at L0; with parents (int32 [B,T]) a node's position is
     its depth in the tree past that.  Yq [B*T, Hq*d], Yk and Yv [B*T, Hkv*d].  Returns Q."""
+    rc = _short().qkv_rope(Yq, Yk, Yv, Q, Kt, V, lens, L0, parents, q_norm, k_norm, eps, inv_freq, interleaved,
+                           stream and stream.cuda_stream)
+    if rc is not None:
+        _check(rc, "rmm_qkv_rope")
+        return Q
     _dims(Q, "Q", 4)
     B, Hq, T, d = Q.shape
     Bk, Hkv, dk, ldL = _caches(Kt, V)
@@ -629,6 +652,12 @@ def rmm_attn_tree(Q: torch.Tensor, Kt: torch.Tensor, V: torch.Tensor, lens: torc
     sequence's lens[b] cached keys and the node's own ancestors, whose keys sit at the slots lens[b] + node.
     Q [B,Hq,T,d]; Kt [B,Hkv,d,ldL]; V [B,Hkv,ldL,d]; lens int32 [B] (negative: an empty slot, O = 0);
     idx_out (optional) int32 with room for [B, Hkv, ceil(r*d)]."""
+    if O is not None and workspace is not None and opts is None:
+        rc = _short().attn_tree(Q, Kt, V, lens, r, parents, 1.0 / math.sqrt(Q.shape[-1]) if scale is None else scale, O,
+                                idx_out, workspace, stream and stream.cuda_stream)
+        if rc is not None:
+            _check(rc, "rmm_attn_tree")
+            return O
     _dims(Q, "Q", 4)
     B, Hq, T, d = Q.shape
     Bk, Hkv, dk, ldL = _caches(Kt, V)
@@ -682,6 +711,11 @@ def _node_rows(t, name, B, T, V):
 def rmm_softmax(X: torch.Tensor, temperature: float = 1.0, Y: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """Rows of bf16 logits [rows, V] (row stride free) -> probabilities fp32 at a temperature; 0 is greedy: 1 at
     the lowest index of the row's maximum."""
+    if Y is not None:
+        rc = _short().softmax(X, temperature, Y, stream and stream.cuda_stream)
+        if rc is not None:
+            _check(rc, "rmm_softmax")
+            return Y
     ldx = _rows(X, "X", torch.bfloat16)
     rows, V = X.shape
     ldy = _rows(Y, "Y", torch.float32, rows, V) if Y is not None else V
@@ -699,6 +733,11 @@ def rmm_tree_verify(P: torch.Tensor, tokens: torch.Tensor, parents: torch.Tensor
     probabilities P (fp32 [B,T,V], or [B*T,V] with a row stride) with the random numbers u (fp32 [B,T]); Qd, like
     P, are the draft's rows that the children of each node were drawn from (None: certain picks).
     Returns (path [B,T], emitted [B,T], count [B]): the accepted nodes, their tokens and the next one, how many."""
+    if path is not None and emitted is not None and count is not None:
+        rc = _short().tree_verify(P, tokens, parents, u, Qd, path, emitted, count, stream and stream.cuda_stream)
+        if rc is not None:
+            _check(rc, "rmm_tree_verify")
+            return path, emitted, count
     _dims(tokens, "tokens", 2)
     B, T = tokens.shape
     _need(tokens, "tokens", torch.int32)
@@ -727,33 +766,31 @@ def rmm_cache_keep(caches, lens: torch.Tensor, path: torch.Tensor, count: torch.
     """Keep the accepted nodes in every cache (a list of (Kt [B,Hkv,d,ldL], V [B,Hkv,ldL,d]) pairs, one per
     layer): slot lens[b] + path[b,i] moves to lens[b] + i for i < count[b].  Returns lens + count in lens_out
     (new by default; lens itself updates it in place)."""
+    if lens_out is not None:
+        rc = _short().cache_keep(caches, lens, path, count, lens_out, stream and stream.cuda_stream)
+        if rc is not None:
+            _check(rc, "rmm_cache_keep")
+            return lens_out
     caches = list(caches)
     if not caches:
         raise ValueError("no cache given")
     B, Hkv, d, ldL = _caches(*caches[0])
-    bf16, k_shape, v_shape, device = torch.bfloat16, (B, Hkv, d, ldL), (B, Hkv, ldL, d), path.get_device()
-    n = len(caches)
-    kts, vs = [], []
     for Kt, V in caches:
-        if not (Kt.dtype is bf16 and V.dtype is bf16 and Kt.shape == k_shape and V.shape == v_shape
-                and Kt.is_contiguous() and V.is_contiguous()
-                and Kt.get_device() == device and V.get_device() == device):
-            _need(Kt, "Kt", shape=k_shape)
-            _need(V, "V", shape=v_shape)
-            _here("Kt V path", Kt, V, path)
-        kts.append(Kt.data_ptr())
-        vs.append(V.data_ptr())
+        _need(Kt, "Kt", shape=(B, Hkv, d, ldL))
+        _need(V, "V", shape=(B, Hkv, ldL, d))
+        _here("Kt V", Kt, V)
     _dims(path, "path", 2)
     T = path.shape[1]
     _need(path, "path", torch.int32, shape=(B, T))
     _need(lens, "lens", torch.int32, shape=(B,))
     _need(count, "count", torch.int32, shape=(B,))
     _need(lens_out, "lens_out", torch.int32, shape=(B,))
-    dev = _here("path lens count lens_out", path, lens, count, lens_out)  # and with path the caches
+    dev = _here("path lens count lens_out", path, lens, count, lens_out)
     if lens_out is None:
         lens_out = _new((B,), torch.int32, lens, stream)
-    both = array.array("Q", kts + vs)  # the pointers, read during the call
-    base = both.buffer_info()[0]
-    _check(lib().rmm_cache_keep(n, base, base + 8 * n, B, Hkv, d, ldL, _ptr(lens), _ptr(path), _ptr(count), T,
-                                _ptr(lens_out), _stream(stream, dev)), "rmm_cache_keep")
+    n = len(caches)
+    kt = (ctypes.c_void_p * n)(*[Kt.data_ptr() for Kt, _ in caches])
+    v = (ctypes.c_void_p * n)(*[V.data_ptr() for _, V in caches])
+    _check(lib().rmm_cache_keep(n, kt, v, B, Hkv, d, ldL, _ptr(lens), _ptr(path), _ptr(count), T, _ptr(lens_out),
+                                _stream(stream, dev)), "rmm_cache_keep")
     return lens_out

@@ -512,3 +512,60 @@ def test_cache_keep(rmm, B, T, Hkv, ldL, n, in_place):
     assert (out is ln) == in_place
     if not in_place:
         assert torch.equal(ln.cpu(), lens)
+
+
+# ---------------------------------------------------------------- the calls themselves
+
+def test_the_short_way_and_the_long_way_agree(rmm, monkeypatch):
+    """The compiled module in front of the calls and the binding's own marshalling: the same results and the
+    same refusals, on the current stream and a given one."""
+    B, T, Hq, Hkv, ldL, V = 2, 6, 4, 2, 64, 500
+    ys = cuda(*(normal(i, B * T, h * D) for i, h in ((1, Hq), (2, Hkv), (3, Hkv))))
+    lens = torch.tensor([3, 40], dtype=torch.int32, device="cuda")
+    parents = ref.random_trees(B, T, 3).cuda()
+    freq = (10000.0 ** (-torch.arange(0, D, 2, dtype=torch.float32) / D)).cuda()
+    P, tokens, _, u, Qd = cuda(*verify_inputs(B, T, V, 5))
+    X = normal(9, B * T, V).cuda()
+    new = lambda *s, dtype=torch.int32: torch.full(s, -7, device="cuda").to(dtype)
+
+    def run(stream):
+        Q, O = new(B, Hq, T, D, dtype=torch.bfloat16), new(B, Hq, T, D, dtype=torch.bfloat16)
+        caches = [(new(B, Hkv, D, ldL, dtype=torch.bfloat16), new(B, Hkv, ldL, D, dtype=torch.bfloat16)) for _ in range(3)]
+        idx, Y = new(B, Hkv, 64), new(B * T, V, dtype=torch.float32)
+        path, emitted, count, grown = new(B, T), new(B, T), new(B), new(B)
+        ws = rmm.new_workspace(rmm.rmm_attn_tree_workspace_bytes(B, Hq, Hkv, T, ldL))
+        if stream is not None:
+            stream.wait_stream(torch.cuda.current_stream())
+        kw = dict(stream=stream)
+        for kt, v in caches:
+            rmm.rmm_qkv_rope(*ys, Q, kt, v, lens=lens, parents=parents, inv_freq=freq, interleaved=True, **kw)
+        rmm.rmm_attn_tree(Q, *caches[0], lens, 0.5, parents=parents, O=O, idx_out=idx, workspace=ws, **kw)
+        rmm.rmm_softmax(X, 0.8, Y=Y, **kw)
+        rmm.rmm_tree_verify(Y, tokens, parents, u, Qd=Qd, path=path, emitted=emitted, count=count, **kw)
+        rmm.rmm_cache_keep(caches, lens, path, count, lens_out=grown, **kw)
+        torch.cuda.synchronize()
+        with pytest.raises(ValueError, match="emitted"):
+            rmm.rmm_tree_verify(Y, tokens, parents, u, Qd=Qd, path=path, emitted=emitted[:, :-1], count=count)
+        with pytest.raises(ValueError, match="Kt"):
+            rmm.rmm_cache_keep([(caches[0][0][..., :-8], caches[0][1])], lens, path, count, lens_out=grown)
+        with pytest.raises(ValueError, match="Yk"):
+            rmm.rmm_qkv_rope(ys[0], ys[1].float(), ys[2], Q, *caches[0], lens=lens)
+        with pytest.raises(rmm.RmmError):
+            rmm.rmm_softmax(X, -1.0, Y=Y)
+        with pytest.raises(rmm.RmmError):
+            rmm.rmm_attn_tree(Q, *caches[0], lens, 0.5, O=O, workspace=ws[:256])
+        return [Q, O, idx, Y, path, emitted, count, grown] + [t for c in caches for t in c]
+
+    want = run(None)
+    assert int(want[6].min()) >= 0 and bool((want[7] != -7).all())
+    got = [run(torch.cuda.Stream())]
+
+    class Nothing:
+        def __getattr__(self, name):
+            return lambda *a: None
+
+    monkeypatch.setattr(rmm, "_short", Nothing)
+    got += [run(None), run(torch.cuda.Stream())]
+    for g in got:
+        for a, b in zip(g, want):
+            assert torch.equal(a, b)
