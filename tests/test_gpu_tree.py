@@ -176,6 +176,8 @@ ATTN = [  # B, T, Hq, Hkv, lens, ldL, r, tree
     (1, 4, 32, 1, [333], 344, 1.0, "full"),                # one KV head for 32 query heads
     (40, 1, 8, 2, list(range(0, 160, 4)), 168, 1.0, None),  # many short sequences
     (1, 16, 32, 8, [5000], 5016, 0.5, "full"),             # one long sequence over the whole GPU
+    (40, 3, 8, 4, list(range(10, 410, 10)), 416, 0.4, "padded"),  # more heads of keys than the GPU has SMs
+    (2, 25, 10, 1, [77, 900], 960, 0.6, "padded"),         # 250 rows: two tiles, the dims of one unit
 ]
 
 
