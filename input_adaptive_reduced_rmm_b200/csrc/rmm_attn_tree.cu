@@ -69,6 +69,7 @@ constexpr float kRescaleLog2 = 8.0f;
 // a CTA gets (every dim kept, us for 32 x 8k decode: 112 without, 104 at 3, 103 at 6, 104 at 10;
 // fewer kept, tree of 25 over 8 x 16k: 79 without, 73.5 at 3, 71.5 at 6, 70 at 10).
 __host__ __device__ constexpr int piece_cost(bool all) { return all ? 6 : 10; }
+constexpr int kMaxSide = 8;
 constexpr int kSmemMax = 232448;  // 227 KB
 
 struct __align__(8) TreeBars {
@@ -92,6 +93,7 @@ struct TreeArgs {
     long long* cum;  // [B + 1]: cost of the sequences before b; then how many shares, and the cost of a piece
     int* status;
     int B, Hkv, G, T, ldL, R, nrt, nrp, k, kp, nk, nv, slot_rows;
+    int side, U;  // row pairs that CTAs of their own take side by side (or 1), units of a sequence then
     int identity;    // every dim kept
     float scale_log2;
 };
@@ -100,6 +102,10 @@ __device__ __forceinline__ int blocks_of(const TreeArgs& a, int b) {
     const int len = __ldcg(a.lens + b);
     return len < 0 || len > a.ldL - a.T ? 0 : (len + a.T + BK - 1) / BK;
 }
+
+// KV head and row pair of unit u of a sequence.
+__device__ __forceinline__ int head_of(const TreeArgs& a, int u) { return a.side > 1 ? u : u / a.nrp; }
+__device__ __forceinline__ int pair_of(const TreeArgs& a, int u) { return a.side > 1 ? blockIdx.x % a.side : u % a.nrp; }
 
 // A CTA's share as its roles walk it, one piece of a unit at a time.  A unit of nb blocks
 // costs nb + piece: the places [0, piece) stand for the start and end of its pieces, place
@@ -115,7 +121,7 @@ struct Share {
             left -= cost;
             if (left <= 0) return false;
             x = 0;
-            if (++u == a.Hkv * a.nrp) {
+            if (++u == a.U) {
                 u = 0;
                 do nb = blocks_of(a, ++b);
                 while (nb == 0);  // left > 0: a later sequence has blocks
@@ -311,14 +317,15 @@ __global__ void __launch_bounds__(tree_threads(kAll), 1)
     if (warp == 0) {
         // the CTA's share of the whole cost, and where it starts; the last CTA also leaves the
         // running costs for the joining kernel
-        const int U = a.Hkv * a.nrp, c = blockIdx.x;
+        const int U = a.U, c = blockIdx.x / a.side;
+        const bool last = blockIdx.x == gridDim.x - 1;
         long long blocks = 0, seqs = 0;
         const int mine = lane < a.B ? blocks_of(a, lane) : 0;  // of the first 32 sequences
         for (int b = lane; b < a.B; b += 32) {
             const int nb = b == lane ? mine : blocks_of(a, b);
             blocks += nb;
             seqs += nb > 0;
-            if (c == 0 && __ldcg(a.lens + b) > a.ldL - a.T) record_status(status, RMM_ERR_INVALID_ARG);
+            if (blockIdx.x == 0 && __ldcg(a.lens + b) > a.ldL - a.T) record_status(status, RMM_ERR_INVALID_ARG);
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) {
@@ -326,7 +333,7 @@ __global__ void __launch_bounds__(tree_threads(kAll), 1)
             seqs += __shfl_xor_sync(0xffffffffu, seqs, o);
         }
         // shares of more than piece_cost + 1, and never more of them than blocks: none is empty
-        const long long C = min((long long)gridDim.x, blocks * U);
+        const long long C = min((long long)(gridDim.x / a.side), blocks * U);
         const int piece = blocks * U >= C * (2 * piece_cost(kAll)) ? piece_cost(kAll) : 0;
         const long long total = (blocks + seqs * piece) * U;
         const long long p0 = c < C ? total * c / C : total, p1 = c < C ? total * (c + 1) / C : total;
@@ -342,7 +349,7 @@ __global__ void __launch_bounds__(tree_threads(kAll), 1)
                 if (lane >= o) end += v;
             }
             end += base;
-            if (c == (int)gridDim.x - 1 && b < a.B) {
+            if (last && b < a.B) {
                 a.cum[b + 1] = end;
                 if (b == 0) a.cum[0] = 0;
             }
@@ -357,7 +364,7 @@ __global__ void __launch_bounds__(tree_threads(kAll), 1)
         if (lane == 0) {
             bars->cost = (int)(p1 - p0);
             bars->piece = piece;
-            if (c == (int)gridDim.x - 1) a.cum[a.B + 1] = C, a.cum[a.B + 2] = piece;
+            if (last) a.cum[a.B + 1] = C, a.cum[a.B + 2] = piece;
         }
     }
     tc_fence_before();
@@ -388,7 +395,7 @@ __global__ void __launch_bounds__(tree_threads(kAll), 1)
         };
         // the tree and the query operand of the piece at `w`
         auto open = [&]() {
-            const int rp = w.u % a.nrp, plane = w.b * a.Hkv + w.u / a.nrp;
+            const int rp = pair_of(a, w.u), plane = w.b * a.Hkv + head_of(a, w.u);
             const int tiles = 2 * rp + 1 < a.nrt ? 2 : 1;
             const size_t row0 = (size_t)plane * a.R;
             if (a.parents && tid < a.T) par[tid] = __ldcg(a.parents + (size_t)w.b * a.T + tid);
@@ -462,7 +469,7 @@ __global__ void __launch_bounds__(tree_threads(kAll), 1)
         bool more = w.next(a, bars, true);
         if (more) open();
         for (; ok && more; ++piece) {
-            const int g = w.u / a.nrp, rp = w.u % a.nrp;
+            const int g = head_of(a, w.u), rp = pair_of(a, w.u);
             const bool two = 2 * rp + 1 < a.nrt;
             const int plane = w.b * a.Hkv + g;
             const int len = __ldcg(a.lens + w.b);
@@ -668,7 +675,7 @@ __global__ void __launch_bounds__(tree_threads(kAll), 1)
                 Ring k, v;
                 bool ok = true;
                 for (bool more = w.next(a, bars, true); ok && more; more = w.next(a, bars, false)) {
-                    const int plane = w.b * a.Hkv + w.u / a.nrp;
+                    const int plane = w.b * a.Hkv + head_of(a, w.u);
                     for (int j = 0; j < w.n; ++j, ++c) {
                         const int key0 = (w.blk + j) * BK;
                         if (kAll) {
@@ -721,7 +728,7 @@ __global__ void __launch_bounds__(tree_threads(kAll), 1)
             bool ok = true;
             for (bool more = w.next(a, bars, true); ok && more; more = w.next(a, bars, false), ++piece) {
                 // with two row tiles every block is this group's, with one every second
-                const bool two = 2 * (w.u % a.nrp) + 1 < a.nrt;
+                const bool two = 2 * pair_of(a, w.u) + 1 < a.nrt;
                 const int by = two ? 1 : 2, steps = two ? w.n : (w.n + 1 - g) / 2;
                 const int releases = two ? 1 : users;  // the group alone releases a block of one tile
                 const uint64_t qd = qd0 + (uint64_t)((two ? g : 0) * (Q_BYTES / 16));  // descriptors count 16 bytes
@@ -792,7 +799,7 @@ __global__ void __launch_bounds__(tree_threads(kAll), 1)
         Ring k;
         bool ok = true;
         for (bool more = w.next(a, bars, true); ok && more; more = w.next(a, bars, false)) {
-            const int plane = w.b * a.Hkv + w.u / a.nrp;
+            const int plane = w.b * a.Hkv + head_of(a, w.u);
             uint32_t at[8];  // the rows' places in the d-major cache; the padding repeats a kept row
 #pragma unroll
             for (int i = 0; i < 8; ++i)
@@ -835,8 +842,9 @@ constexpr int kJoinThreads = 256;
 template <int kLanes>
 __global__ void __launch_bounds__(kJoinThreads) attn_tree_join_kernel(const TreeArgs a) {
     constexpr int kRows = kJoinThreads / 32 / kLanes, kFly = 4;
-    const int U = a.Hkv * a.nrp, z = threadIdx.x % kLanes, tid = threadIdx.x / kLanes;
-    const int unit = blockIdx.x, b = unit / U, u = unit % U, g = u / a.nrp, rp = u % a.nrp;
+    const int U = a.U, z = threadIdx.x % kLanes, tid = threadIdx.x / kLanes;
+    const int plane = blockIdx.x / a.nrp, rp = blockIdx.x % a.nrp, b = plane / a.Hkv, g = plane % a.Hkv;
+    const int u = a.side > 1 ? g : g * a.nrp + rp;
     const int r = blockIdx.y * kRows + tid % kRows, c4 = tid / kRows;
     pdl_wait();
     pdl_launch_dependents();
@@ -851,7 +859,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_tree_join_kernel(const Tree
     const size_t sf = slot_floats(a.slot_rows);
     // the first share may have begun with another unit: its piece is then its second
     const int skip = nb && total * c0 / C < p0 ? 1 : 0;
-    const float* base = a.partials + (size_t)(2 * c0) * sf;
+    const float* base = a.partials + (size_t)(2 * (c0 * a.side + (a.side > 1 ? rp : 0))) * sf;
     const size_t at = ((size_t)c4 * a.slot_rows + row) * 4;
     float M = -INFINITY, L = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -863,7 +871,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_tree_join_kernel(const Tree
             const int j = i0 + i * kLanes;
             m[i] = -INFINITY;
             if (j < n) {
-                const float* p = base + (size_t)(2 * j + (j == 0 ? skip : 0)) * sf;
+                const float* p = base + (size_t)(2 * j * a.side + (j == 0 ? skip : 0)) * sf;
                 m[i] = p[D * a.slot_rows + row];
                 l[i] = p[(D + 1) * a.slot_rows + row];
                 v[i] = *reinterpret_cast<const float4*>(p + at);
@@ -1020,6 +1028,11 @@ cudaError_t launch_attn_tree(const CUtensorMap& qmap, const CUtensorMap& kmap, c
     a.status = status;
     a.B = B, a.Hkv = Hkv, a.G = Hq / Hkv, a.T = T, a.ldL = ldL;
     a.R = p.R, a.nrt = p.nrt, a.nrp = p.nrp, a.slot_rows = p.slot_rows;
+    // Row pairs of a head that CTAs take side by side read its keys and values at the same time, so
+    // that L2 serves all but the first (64 nodes of 8 heads over 32k keys, 262 us against 279 with
+    // the pairs one after the other); a head with more pairs than this has enough work of its own.
+    a.side = p.nrp <= kMaxSide && p.nrp <= p.ctas ? p.nrp : 1;
+    a.U = Hkv * p.nrp / a.side;
     a.k = k;
     a.kp = (k + 15) / 16 * 16;
     a.scale_log2 = scale * 1.4426950408889634f;
