@@ -8,17 +8,18 @@
 //   softmax_kernel       a row in the registers of a cluster of 1, 2, 4 or 8 CTAs,
 //                        read once: the shortest way for one row, but every CTA of
 //                        the SM loads, exchanges and stores at the same time
-//   softmax_rows_kernel  a row in parts over 4 small CTAs, read twice (the second
-//                        time from L2): five CTAs per SM in different phases
+//   softmax_rows_kernel  a row in parts over 4 or 8 small CTAs of 128 threads, each part
+//                        copied to shared memory at once and read there twice: six CTAs
+//                        per SM in different phases
 // Measured, us for (rows, V), registers against parts:
-//   (16, 32000) 5.5 4.2   (32, 16384) 4.5 4.1   (32, 131072) 12.9 14.6
-//   (64, 4096) 2.4 3.8    (64, 8192) 4.1 4.0    (64, 32000) 13.6 7.3
-//   (512, 8192) 15.1 17.3 (512, 16384) 29.6 20.9   (512, 131072) 158 97
+//   (16, 32000) 5.1 4.2   (32, 16384) 4.2 4.3     (32, 131072) 10.4 10.1
+//   (64, 8192) 3.9 4.2    (64, 32000) 12.5 6.0    (512, 8192) 13.1 12.1
+//   (512, 16384) 25.9 16.0                        (512, 131072) 126 75
 // so parts are taken from 32 rows of 16384 logits on, where rows start on 16-byte
-// boundaries.  (512, 131072) moves 4.15 TB/s of its 403 MB; the two exponentials
-// per element take 35 us of it, the wait for the cluster and uneven phases the rest.
-// A wave of resident clusters over many rows (169 us) and 8 or 16 vectors in
-// flight per thread (109, 126) were slower.
+// boundaries.  (512, 131072) moves its 403 MB at 5.4 TB/s; the two exponentials per
+// element take 35 us beside that.  Slower at 512 x 131072 were a second read from L2
+// instead of shared memory (80), two 16-byte stores instead of one of 32 (99) and a
+// wave of resident clusters over many rows (169).
 #include <math.h>
 
 #include "rmm_common.cuh"
@@ -29,10 +30,12 @@ namespace rmm {
 namespace {
 
 constexpr int kThreads = 512;
-// softmax_rows_kernel: when it is taken, its threads, CTAs per SM, CTAs per row and
-// vectors in flight (us at 512 x 131072: 97; 6 CTAs 109, 2 vectors 105, 8 parts 111)
+// softmax_rows_kernel: when it is taken, its threads, CTAs per SM and vectors of a thread
+// at a time, and the length from which a row has 8 parts instead of 4 (us, 4 against 8 parts:
+// 23.6 and 28.1 at 512 x 32000, 80.8 and 75.5 at 512 x 131072; 256 threads 28.5 and 79.8).
 constexpr int kManyRows = 32, kLongRow = 16384;
-constexpr int kRowThreads = 256, kRowCtas = 5, kParts = 4, kRowFly = 4;
+constexpr int kRowThreads = 128, kRowCtas = 6, kRowFly = 4;
+constexpr int kEightParts = 65536;
 constexpr float kLog2e = 1.4426950408889634f;
 
 __device__ __forceinline__ float ld_shared_cluster_f32(uint32_t addr) {
@@ -62,8 +65,27 @@ __device__ __forceinline__ void merge(float& m, float& s, float m2, float s2, fl
     s = a + b;
 }
 
+// Eight outputs as one 32-byte store: two of 16 bytes leave every sector half written twice, which
+// cost a quarter of the time (512 x 131072: 99 us, 80 with whole sectors).
+__device__ __forceinline__ void store8(float* d, const float (&p)[8], bool whole) {
+    if (whole) {
+        asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(d), "f"(p[0]), "f"(p[1]),
+                     "f"(p[2]), "f"(p[3]), "f"(p[4]), "f"(p[5]), "f"(p[6]), "f"(p[7])
+                     : "memory");
+    } else {
+        reinterpret_cast<float4*>(d)[0] = make_float4(p[0], p[1], p[2], p[3]);
+        reinterpret_cast<float4*>(d)[1] = make_float4(p[4], p[5], p[6], p[7]);
+    }
+}
+
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int n>
+__device__ __forceinline__ void cp_async_wait_but() {  // all but the last n groups
+    asm volatile("cp.async.wait_group %0;" ::"n"(n) : "memory");
+}
+
 // NV: 16-byte vectors (8 logits) per thread.  wide: rows of X start on 16-byte
-// boundaries; wide_y: rows of Y do.
+// boundaries; wide_y: rows of Y do (2: on 32-byte boundaries).
 template <int NV>
 __global__ void __launch_bounds__(kThreads)
     softmax_kernel(const uint16_t* X, int V, int64_t ldx, float c, int one_hot, float* Y,
@@ -179,8 +201,7 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
         for (int e = 0; e < 8; ++e) p[e] = ex2((at(i, e) - ref_row) * c) * inv;
         if (wide_y && e0 + 8 <= V) {
-            *reinterpret_cast<float4*>(y + e0) = make_float4(p[0], p[1], p[2], p[3]);
-            *reinterpret_cast<float4*>(y + e0 + 4) = make_float4(p[4], p[5], p[6], p[7]);
+            store8(y + e0, p, wide_y > 1);
         } else {
 #pragma unroll
             for (int e = 0; e < 8; ++e)
@@ -191,55 +212,70 @@ __global__ void __launch_bounds__(kThreads)
 
 __device__ __forceinline__ __nv_bfloat162 pair(uint32_t w) { return *reinterpret_cast<const __nv_bfloat162*>(&w); }
 
-// A part of a row per CTA (a cluster of kParts), read twice: for the maximum and the
-// sum, then for the probabilities.  Stores bypass the caches' lasting part so that the
-// second read still hits L2 (107 us without, 98 with).
+// A part of a row per CTA (a cluster of kParts), all of it on its way to shared memory at
+// once: the maximum and the sum as the groups of copies land, the probabilities from there.
+// A thread reads only what it copied.
+template <int kParts>
 __global__ void __launch_bounds__(kRowThreads, kRowCtas)
-    softmax_rows_kernel(const uint16_t* X, int V, int64_t ldx, float c, float* Y, int64_t ldy) {
+    softmax_rows_kernel(const uint16_t* X, int V, int64_t ldx, float c, float* Y, int64_t ldy, int per, bool whole) {
+    extern __shared__ uint4 held[];
     __shared__ float red_m[kRowThreads / 32], red_s[kRowThreads / 32];
     __shared__ float part[2];
-    constexpr int kFly = kRowFly;
+    constexpr int kGroups = 4, kStep = kRowFly * kRowThreads;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int64_t row = blockIdx.x / kParts;
     const int rank = blockIdx.x % kParts;
-    const int vecs = V / 8, per = (vecs / kParts + 32) & ~31;
-    const int lo = rank * per, hi = min(vecs, lo + per);
-    const bool tail = rank == kParts - 1 && vecs * 8 + tid < V;  // the last, partial vector
-    const uint16_t* x = X + row * ldx;
-    float* y = Y + row * ldy;
+    const int vecs = V / 8, lo = rank * per, n = min(vecs - lo, per);  // this CTA's vectors
+    const bool tail = rank == kParts - 1 && vecs * 8 + tid < V;        // the last, partial vector
+    const uint16_t* x = X + row * ldx + (int64_t)lo * 8;
+    float* y = Y + row * ldy + (int64_t)lo * 8;
+    const int group = (per + kGroups * kStep - 1) / (kGroups * kStep) * kStep;
     pdl_wait();
     pdl_launch_dependents();
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g) {
+        for (int i = g * group + tid; i < min(n, (g + 1) * group); i += kRowThreads)
+            cp_async_16(smem_addr(held + i), x + (int64_t)i * 8, 16);
+        cp_async_commit();
+    }
     auto at = [](const uint4& r, int e) -> float {
         const uint32_t w = e < 2 ? r.x : e < 4 ? r.y : e < 6 ? r.z : r.w;
         return __uint_as_float((e & 1) ? w & 0xFFFF0000u : w << 16);
     };
     float m = -INFINITY, s = 0.f;
-    for (int i0 = lo + tid; i0 < hi; i0 += kFly * kRowThreads) {
-        uint4 r[kFly];
 #pragma unroll
-        for (int i = 0; i < kFly; ++i)
-            r[i] = i0 + i * kRowThreads < hi ? *reinterpret_cast<const uint4*>(x + (int64_t)(i0 + i * kRowThreads) * 8)
-                                          : make_uint4(0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u);
-        // the maximum in pairs, as bf16 (exact)
-        __nv_bfloat162 top = pair(r[0].x);
+    for (int g = 0; g < kGroups; ++g) {
+        if (g == 0) cp_async_wait_but<3>();
+        if (g == 1) cp_async_wait_but<2>();
+        if (g == 2) cp_async_wait_but<1>();
+        if (g == 3) cp_async_wait_but<0>();
+        for (int i0 = g * group + tid; i0 < min(n, (g + 1) * group); i0 += kStep) {
+            uint4 r[kRowFly];
 #pragma unroll
-        for (int i = 0; i < kFly; ++i) {
-            top = __hmax2(top, __hmax2(pair(r[i].x), pair(r[i].y)));
-            top = __hmax2(top, __hmax2(pair(r[i].z), pair(r[i].w)));
+            for (int i = 0; i < kRowFly; ++i)
+                r[i] = i0 + i * kRowThreads < n ? held[i0 + i * kRowThreads]
+                                                : make_uint4(0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u);
+            // the maximum in pairs, as bf16 (exact)
+            __nv_bfloat162 top = pair(r[0].x);
+#pragma unroll
+            for (int i = 0; i < kRowFly; ++i) {
+                top = __hmax2(top, __hmax2(pair(r[i].x), pair(r[i].y)));
+                top = __hmax2(top, __hmax2(pair(r[i].z), pair(r[i].w)));
+            }
+            const float mm = fmaxf(m, fmaxf(__low2float(top), __high2float(top)));
+            if (mm > m) {
+                s *= ex2((m - mm) * c);
+                m = mm;
+            }
+            const float ref = reference(m);
+#pragma unroll
+            for (int i = 0; i < kRowFly; ++i)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) s += ex2((at(r[i], e) - ref) * c);
         }
-        const float mm = fmaxf(m, fmaxf(__low2float(top), __high2float(top)));
-        if (mm > m) {
-            s *= ex2((m - mm) * c);
-            m = mm;
-        }
-        const float ref = reference(m);
-#pragma unroll
-        for (int i = 0; i < kFly; ++i)
-#pragma unroll
-            for (int e = 0; e < 8; ++e) s += ex2((at(r[i], e) - ref) * c);
     }
     if (tail) {
-        const float v = __uint_as_float((uint32_t)x[vecs * 8 + tid] << 16);
+        const float v = __uint_as_float((uint32_t)X[row * ldx + vecs * 8 + tid] << 16);
         merge(m, s, fmaxf(v, -INFINITY), ex2((v - reference(v)) * c), c);
     }
 #pragma unroll
@@ -263,25 +299,23 @@ __global__ void __launch_bounds__(kRowThreads, kRowCtas)
         merge(m, s, ld_shared_cluster_f32(mapa_shared(smem_addr(&part[0]), j)),
               ld_shared_cluster_f32(mapa_shared(smem_addr(&part[1]), j)), c);
     const float inv = s == 0.0f ? 0.0f : 1.0f / s, ref = reference(m);
-    for (int i0 = lo + tid; i0 < hi; i0 += kFly * kRowThreads) {
-        uint4 r[kFly];
+    for (int i0 = tid; i0 < n; i0 += kStep) {
+        uint4 r[kRowFly];
 #pragma unroll
-        for (int i = 0; i < kFly; ++i)
-            if (i0 + i * kRowThreads < hi) r[i] = *reinterpret_cast<const uint4*>(x + (int64_t)(i0 + i * kRowThreads) * 8);
+        for (int i = 0; i < kRowFly; ++i)
+            if (i0 + i * kRowThreads < n) r[i] = held[i0 + i * kRowThreads];
 #pragma unroll
-        for (int i = 0; i < kFly; ++i) {
-            if (i0 + i * kRowThreads >= hi) break;
+        for (int i = 0; i < kRowFly; ++i) {
+            if (i0 + i * kRowThreads >= n) break;
             float p[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) p[e] = ex2((at(r[i], e) - ref) * c) * inv;
-            float4* d = reinterpret_cast<float4*>(y + (int64_t)(i0 + i * kRowThreads) * 8);
-            __stcs(d, make_float4(p[0], p[1], p[2], p[3]));
-            __stcs(d + 1, make_float4(p[4], p[5], p[6], p[7]));
+            store8(y + (int64_t)(i0 + i * kRowThreads) * 8, p, whole);
         }
     }
     if (tail) {
-        const float v = __uint_as_float((uint32_t)x[vecs * 8 + tid] << 16);
-        y[vecs * 8 + tid] = ex2((v - ref) * c) * inv;
+        const float v = __uint_as_float((uint32_t)X[row * ldx + vecs * 8 + tid] << 16);
+        Y[row * ldy + vecs * 8 + tid] = ex2((v - ref) * c) * inv;
     }
     cluster_sync();  // no CTA leaves while another still reads its pair
 }
@@ -290,7 +324,9 @@ template <int NV>
 cudaError_t launch(const uint16_t* X, int rows, int V, int64_t ldx, float temperature, float* Y, int64_t ldy, int nc,
                    cudaStream_t stream) {
     const int wide = (reinterpret_cast<uintptr_t>(X) & 15) == 0 && ldx % 8 == 0;
-    const int wide_y = (reinterpret_cast<uintptr_t>(Y) & 15) == 0 && ldy % 4 == 0;
+    const int wide_y = (reinterpret_cast<uintptr_t>(Y) & 31) == 0 && ldy % 8 == 0   ? 2
+                       : (reinterpret_cast<uintptr_t>(Y) & 15) == 0 && ldy % 4 == 0 ? 1
+                                                                                    : 0;
     const int one_hot = temperature == 0.0f;
     const float c = one_hot ? 0.0f : kLog2e / temperature;
     cudaLaunchConfig_t cfg = {};
@@ -309,6 +345,30 @@ cudaError_t launch(const uint16_t* X, int rows, int V, int64_t ldx, float temper
     return cudaLaunchKernelEx(&cfg, softmax_kernel<NV>, X, V, ldx, c, one_hot, Y, ldy, nc, wide, wide_y);
 }
 
+template <int kParts>
+cudaError_t launch_rows(const uint16_t* X, int rows, int V, int64_t ldx, float temperature, float* Y, int64_t ldy,
+                        cudaStream_t stream) {
+    const int per = (V / 8 / kParts + 32) & ~31;  // vectors of a part, the last one's fewer
+    const bool whole = (reinterpret_cast<uintptr_t>(Y) & 31) == 0 && ldy % 8 == 0;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)rows * kParts);
+    cfg.blockDim = dim3(kRowThreads);
+    cfg.dynamicSmemBytes = (size_t)per * 16;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = kParts;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    const cudaError_t e = ensure_smem_limit(softmax_rows_kernel<kParts>, cfg.dynamicSmemBytes);
+    if (e != cudaSuccess) return e;
+    return cudaLaunchKernelEx(&cfg, softmax_rows_kernel<kParts>, X, V, ldx, kLog2e / temperature, Y, ldy, per, whole);
+}
+
 }  // namespace
 
 cudaError_t launch_softmax(const uint16_t* X, int rows, int V, int64_t ldx, float temperature, float* Y, int64_t ldy,
@@ -316,22 +376,9 @@ cudaError_t launch_softmax(const uint16_t* X, int rows, int V, int64_t ldx, floa
     const int vecs = (V + 7) / 8;
     const bool aligned = (reinterpret_cast<uintptr_t>(X) & 15) == 0 && ldx % 8 == 0 &&
                          (reinterpret_cast<uintptr_t>(Y) & 15) == 0 && ldy % 4 == 0;
-    if (aligned && temperature != 0.0f && rows >= kManyRows && V >= kLongRow) {
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3((unsigned)rows * kParts);
-        cfg.blockDim = dim3(kRowThreads);
-        cfg.stream = stream;
-        cudaLaunchAttribute attr[2];
-        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr[0].val.programmaticStreamSerializationAllowed = 1;
-        attr[1].id = cudaLaunchAttributeClusterDimension;
-        attr[1].val.clusterDim.x = kParts;
-        attr[1].val.clusterDim.y = 1;
-        attr[1].val.clusterDim.z = 1;
-        cfg.attrs = attr;
-        cfg.numAttrs = 2;
-        return cudaLaunchKernelEx(&cfg, softmax_rows_kernel, X, V, ldx, kLog2e / temperature, Y, ldy);
-    }
+    if (aligned && temperature != 0.0f && rows >= kManyRows && V >= kLongRow)
+        return V >= kEightParts ? launch_rows<8>(X, rows, V, ldx, temperature, Y, ldy, stream)
+                                : launch_rows<4>(X, rows, V, ldx, temperature, Y, ldy, stream);
     int nc = 1;
     while (nc < 8 && vecs > nc * kThreads) nc *= 2;
     const int nv = (vecs + nc * kThreads - 1) / (nc * kThreads);

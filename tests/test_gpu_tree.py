@@ -289,6 +289,21 @@ def test_softmax(rmm, rows, V, t):
     within(rmm.rmm_softmax(X.cuda(), t), want, softmax_tol(x, t, want), "Y")
 
 
+@pytest.mark.parametrize("rows,V,ldx,ldy", [(32, 16384, 16384, 16384), (33, 16391, 16392, 16396), (40, 20000, 20008, 20008),
+                                            (32, 65543, 65544, 65544), (35, 131072, 131072, 131076),
+                                            (32, 262144, 262144, 262144)])
+def test_softmax_many_long_rows(rmm, rows, V, ldx, ldy):
+    X = normal(V, rows, ldx, std=3.0)
+    X[1, : V - 4] = -math.inf  # mass in the last part alone
+    X[2, 5:V] = -math.inf
+    Y = torch.full((rows, ldy), 5.0, device="cuda")
+    rmm.rmm_softmax(X.cuda()[:, :V], 0.9, Y=Y[:, :V])
+    x = X[:, :V].double()
+    want = torch.softmax(x / 0.9, -1)
+    within(Y[:, :V], want, softmax_tol(x, 0.9, want), "Y")
+    assert bool((Y[:, V:] == 5.0).all())
+
+
 @pytest.mark.parametrize("off,ldx,ldy", [(0, 1008, 1004), (0, 1001, 1001), (1, 1008, 1003), (3, 1007, 1008)])
 def test_softmax_strides(rmm, off, ldx, ldy):
     """Rows of padded logits and padded outputs, aligned and not; the padding is neither read
