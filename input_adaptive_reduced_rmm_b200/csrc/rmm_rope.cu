@@ -114,12 +114,13 @@ __global__ void __launch_bounds__(kRopeThreads, 2) qkv_rope_kernel(const RopeArg
     const int tpar = nt > 16 ? 32 : nt > 8 ? 16 : nt > 4 ? 8 : nt > 2 ? 4 : nt;
     const int hpar = 32 / tpar, ho = qw / tpar;
     const bool turns = kind != 2 && a.inv_freq;
-    // the lane's dims A .. A+7 and B .. B+7: pairs (A + e, B + e), or neighbours when interleaved
+    // the lane's dims A .. A+7 and B .. B+7: pairs (A + e, B + e), or neighbours when interleaved;
+    // a quarter-warp's loads and stores are 128 bytes in a row wherever the pairs allow it
     const int half = a.rot / 2;
-    int A = 16 * l, B = 16 * l + 8;
-    bool turned = turns && A < a.rot;
+    int A = 8 * l, B = 64 + 8 * l;
+    bool turned = turns && A < a.rot, turned_b = turns && B < a.rot;
     if (turns && !kInterleaved) {
-        turned = 8 * l < half;
+        turned = turned_b = 8 * l < half;
         A = turned ? 8 * l : a.rot + 2 * (8 * l - half);
         B = turned ? 8 * l + half : A + 8;
     }
@@ -157,13 +158,14 @@ __global__ void __launch_bounds__(kRopeThreads, 2) qkv_rope_kernel(const RopeArg
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 float c0 = 1.f, s0 = 0.f, c1 = 1.f, s1 = 0.f;
-                if (turned) {
-                    turn(pos, freq[8 * l + 2 * e], c0, s0);
-                    turn(pos, freq[8 * l + 2 * e + 1], c1, s1);
+                // of pairs across a and b, 8 angles for both; of neighbours, 4 of a's and 4 of b's
+                const int at = !kInterleaved ? 8 * l + 2 * e : e < 2 ? 4 * l + 2 * e : 32 + 4 * l + 2 * (e - 2);
+                if (e < 2 ? turned : turned_b) {
+                    turn(pos, freq[at], c0, s0);
+                    turn(pos, freq[at + 1], c1, s1);
                 }
                 if (kInterleaved) {
-                    // angles 2e, 2e+1 of the lane's 8 belong to the neighbours of word pair e: those of a
-                    // for e < 2, of b above; their (c, c) and (-s, s), weights of the partner in the second
+                    // the angles belong to the neighbours of two words: of a for e < 2, of b above; their (c, c) and (-s, s), weights of the partner in the second
                     F2* cx = e < 2 ? ca : cb;
                     F2* sx = e < 2 ? sa : sb;
                     const F2* wx = e < 2 ? wa : wb;
