@@ -726,7 +726,7 @@ rmm_status rmm_qkv_rope(const void* Yq, const void* Yk, const void* Yv, int B, i
         static_cast<const uint16_t*>(Yq), static_cast<const uint16_t*>(Yk), static_cast<const uint16_t*>(Yv), B, T, Hq,
         Hkv, static_cast<const uint16_t*>(q_norm), static_cast<const uint16_t*>(k_norm), eps, inv_freq, rot,
         interleaved ? 1 : 0, lens, L0, parents, static_cast<uint16_t*>(Q), static_cast<uint16_t*>(Kt),
-        static_cast<uint16_t*>(V), ldL, static_cast<cudaStream_t>(stream)));
+        static_cast<uint16_t*>(V), ldL, num_sms_current(), static_cast<cudaStream_t>(stream)));
 }
 
 namespace {

@@ -191,7 +191,7 @@ cudaError_t launch_attn_ctx(const uint16_t* Q, const uint16_t* Kt, const uint16_
 cudaError_t launch_qkv_rope(const uint16_t* Yq, const uint16_t* Yk, const uint16_t* Yv, int B, int T, int Hq, int Hkv,
                             const uint16_t* q_norm, const uint16_t* k_norm, float eps, const float* inv_freq, int rot,
                             int interleaved, const int32_t* lens, int L0, const int32_t* parents, uint16_t* Q,
-                            uint16_t* Kt, uint16_t* V, int ldL, cudaStream_t stream);
+                            uint16_t* Kt, uint16_t* V, int ldL, int num_sms, cudaStream_t stream);
 // Bytes of split partials for these sizes.
 size_t attn_tree_partial_bytes(int B, int Hq, int Hkv, int T, int ldL, int num_sms);
 // qmap: Q as rows of 128 dims, box 64 x 128; kmap: Kt as [plane][dim][key], box 64 keys x 128

@@ -61,6 +61,8 @@ QKV = [  # B, T, Hq, Hkv, lens, ldL, rot, interleaved, norm, tree
     (2, 64, 12, 9, [13, 64], 128, 16, False, True, True),
     (1, 65, 4, 2, [62], 128, 128, False, True, False),      # two token tiles, odd start
     (2, 200, 5, 1, [1, 40], 240, 96, True, True, False),
+    (75, 1, 40, 9, list(range(-1, 74)), 80, 128, False, True, False),  # single tokens, more than the GPU takes at once
+    (150, 1, 8, 8, list(range(150)), 152, 64, True, False, True),
 ]
 
 
