@@ -93,8 +93,15 @@ struct Call {
 
 constexpr at::ScalarType kBf16 = at::kBFloat16, kF32 = at::kFloat, kI32 = at::kInt;
 
-PyObject* finish(const Call& c, rmm_status rc) {
+// The call's status, made without the interpreter's lock (a launch may have to wait for
+// the GPU, and the GPU for a callback that takes the lock); None where `c` is not ok.
+template <typename F>
+PyObject* make(const Call& c, F call) {
     if (!c.ok) Py_RETURN_NONE;
+    rmm_status rc;
+    Py_BEGIN_ALLOW_THREADS;
+    rc = call();
+    Py_END_ALLOW_THREADS;
     return PyLong_FromLong(rc);
 }
 
@@ -141,13 +148,12 @@ PyObject* qkv_rope(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
         const int interleaved = PyObject_IsTrue(a[13]);
         if (interleaved < 0) PyErr_Clear(), c.ok = false;
         const rmm_stream_t s = c.stream(a[14]);
-        rmm_status rc = RMM_OK;
-        if (c.ok)
-            rc = rmm_qkv_rope(Yq, Yk, Yv, (int)B, (int)T, (int)Hq, (int)Hkv, (int)d, qn, kn, (float)eps,
-                              static_cast<const float*>(freq), (int)(2 * f[0]), interleaved,
-                              static_cast<const int32_t*>(lens), (int)L0, static_cast<const int32_t*>(parents), Q, Kt, V,
-                              (int)ldL, s);
-        return finish(c, rc);
+        return make(c, [&] {
+            return rmm_qkv_rope(Yq, Yk, Yv, (int)B, (int)T, (int)Hq, (int)Hkv, (int)d, qn, kn, (float)eps,
+                static_cast<const float*>(freq), (int)(2 * f[0]), interleaved,
+                static_cast<const int32_t*>(lens), (int)L0, static_cast<const int32_t*>(parents), Q, Kt, V,
+                (int)ldL, s);
+        });
     });
 }
 
@@ -180,12 +186,11 @@ PyObject* attn_tree(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
         c.sizes(a[9], w);
         void* ws = c.of(a[9], at::kByte, {w[0]});
         const rmm_stream_t s = c.stream(a[10]);
-        rmm_status rc = RMM_OK;
-        if (c.ok)
-            rc = rmm_attn_tree(Q, Kt, V, static_cast<const int32_t*>(lens), static_cast<const int32_t*>(parents), (int)B,
-                               (int)Hq, (int)Hkv, (int)T, (int)ldL, (int)d, r, (float)scale, O, static_cast<int32_t*>(idx),
-                               ws, (size_t)w[0], s, nullptr);
-        return finish(c, rc);
+        return make(c, [&] {
+            return rmm_attn_tree(Q, Kt, V, static_cast<const int32_t*>(lens), static_cast<const int32_t*>(parents), (int)B,
+                (int)Hq, (int)Hkv, (int)T, (int)ldL, (int)d, r, (float)scale, O, static_cast<int32_t*>(idx),
+                ws, (size_t)w[0], s, nullptr);
+        });
     });
 }
 
@@ -199,9 +204,9 @@ PyObject* softmax(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
         const double t = c.number(a[1]);
         void* Y = c.of(a[2], kF32, {x[0], x[1]});
         const rmm_stream_t s = c.stream(a[3]);
-        rmm_status rc = RMM_OK;
-        if (c.ok) rc = rmm_softmax(X, (int)x[0], (int)x[1], x[1], (float)t, static_cast<float*>(Y), x[1], s);
-        return finish(c, rc);
+        return make(c, [&] {
+            return rmm_softmax(X, (int)x[0], (int)x[1], x[1], (float)t, static_cast<float*>(Y), x[1], s);
+        });
     });
 }
 
@@ -229,13 +234,12 @@ PyObject* tree_verify(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
         void* emitted = c.of(a[6], kI32, {B, T});
         void* count = c.of(a[7], kI32, {B});
         const rmm_stream_t s = c.stream(a[8]);
-        rmm_status rc = RMM_OK;
-        if (c.ok)
-            rc = rmm_tree_verify(P, V, Qd, Qd ? V : 0, (int)B, (int)T, (int)V, static_cast<const int32_t*>(tokens),
-                                 static_cast<const int32_t*>(parents), static_cast<const float*>(u),
-                                 static_cast<int32_t*>(path), static_cast<int32_t*>(emitted), static_cast<int32_t*>(count),
-                                 s);
-        return finish(c, rc);
+        return make(c, [&] {
+            return rmm_tree_verify(P, V, Qd, Qd ? V : 0, (int)B, (int)T, (int)V, static_cast<const int32_t*>(tokens),
+                static_cast<const int32_t*>(parents), static_cast<const float*>(u),
+                static_cast<int32_t*>(path), static_cast<int32_t*>(emitted), static_cast<int32_t*>(count),
+                s);
+        });
     });
 }
 
@@ -261,12 +265,11 @@ PyObject* cache_keep(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
         void* count = c.of(a[3], kI32, {B});
         void* lens_out = c.of(a[4], kI32, {B});
         const rmm_stream_t s = c.stream(a[5]);
-        rmm_status rc = RMM_OK;
-        if (c.ok)
-            rc = rmm_cache_keep((int)layers, Kt.data(), V.data(), (int)B, (int)k[1], (int)k[2], (int)k[3],
-                                static_cast<const int32_t*>(lens), static_cast<const int32_t*>(path),
-                                static_cast<const int32_t*>(count), (int)T, static_cast<int32_t*>(lens_out), s);
-        return finish(c, rc);
+        return make(c, [&] {
+            return rmm_cache_keep((int)layers, Kt.data(), V.data(), (int)B, (int)k[1], (int)k[2], (int)k[3],
+                static_cast<const int32_t*>(lens), static_cast<const int32_t*>(path),
+                static_cast<const int32_t*>(count), (int)T, static_cast<int32_t*>(lens_out), s);
+        });
     });
 }
 

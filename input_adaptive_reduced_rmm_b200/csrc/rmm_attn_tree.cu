@@ -923,11 +923,21 @@ __global__ void __launch_bounds__(256) tree_dims_kernel(const TreeArgs a) {
     __shared__ int32_t par[kTreeMax];
     __shared__ uint64_t there_s;
     __shared__ uint32_t red[16][D];
-    __shared__ uint32_t sv[D];
+    __shared__ __align__(16) uint32_t sv[D];
     __shared__ int warp_cnt[D / 32];
     const int plane = blockIdx.x, b = plane / a.Hkv, tid = threadIdx.x;
     pdl_wait();
     pdl_launch_dependents();
+    const int c16 = tid & 15, rl = tid >> 4;
+    uint32_t m[4] = {0, 0, 0, 0};  // two dims each, magnitudes of 15 bits
+    const uint16_t* q = a.Q + (size_t)plane * a.R * D + c16 * 8;
+    uint4 v[8];  // eight rows in flight, the first while the length and the tree arrive
+    auto fetch = [&](int r0) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            v[i] = r0 + 16 * i < a.R ? ld_nc_v4(q + (size_t)(r0 + 16 * i) * D) : make_uint4(0, 0, 0, 0);
+    };
+    fetch(rl);
     if (blocks_of(a, b) == 0) return;
     uint64_t there = ~0ull;
     if (a.parents) {
@@ -939,14 +949,7 @@ __global__ void __launch_bounds__(256) tree_dims_kernel(const TreeArgs a) {
         __syncthreads();
         there = there_s;
     }
-    const int c16 = tid & 15, rl = tid >> 4;
-    uint32_t m[4] = {0, 0, 0, 0};  // two dims each, magnitudes of 15 bits
-    const uint16_t* q = a.Q + (size_t)plane * a.R * D + c16 * 8;
-    for (int r0 = rl; r0 < a.R; r0 += 128) {  // eight rows in flight
-        uint4 v[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            v[i] = r0 + 16 * i < a.R ? ld_nc_v4(q + (size_t)(r0 + 16 * i) * D) : make_uint4(0, 0, 0, 0);
+    for (int r0 = rl; r0 < a.R; r0 += 128) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const uint32_t keep = (there >> ((r0 + 16 * i) % a.T)) & 1 ? 0x7FFF7FFFu : 0u;  // absent nodes do not count
@@ -955,6 +958,7 @@ __global__ void __launch_bounds__(256) tree_dims_kernel(const TreeArgs a) {
             m[2] = __vmaxu2(m[2], v[i].z & keep);
             m[3] = __vmaxu2(m[3], v[i].w & keep);
         }
+        if (r0 + 128 < a.R) fetch(r0 + 128);
     }
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
@@ -962,18 +966,23 @@ __global__ void __launch_bounds__(256) tree_dims_kernel(const TreeArgs a) {
         red[rl][c16 * 8 + 2 * e + 1] = m[e] >> 16;
     }
     __syncthreads();
-    uint32_t s = 0;
+    // score and, below it, the order of equal ones: no two are the same
+    uint32_t key = 0;
     if (tid < D) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) s = max(s, red[i][tid]);
-        sv[tid] = s;
+        for (int i = 0; i < 16; ++i) key = max(key, red[i][tid]);
+        key = key << 7 | (D - 1 - tid);
+        sv[tid] = key;
     }
     __syncthreads();
     bool keep = false;
     if (tid < D) {
         int rank = 0;
-#pragma unroll 16
-        for (int i = 0; i < D; ++i) rank += sv[i] > s || (sv[i] == s && i < tid);
+#pragma unroll 8
+        for (int i = 0; i < D / 4; ++i) {
+            const uint4 o = reinterpret_cast<const uint4*>(sv)[i];
+            rank += (o.x > key) + (o.y > key) + (o.z > key) + (o.w > key);
+        }
         keep = rank < a.k;
     }
     const unsigned ball = __ballot_sync(0xffffffffu, keep);
