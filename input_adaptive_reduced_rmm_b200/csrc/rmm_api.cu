@@ -20,17 +20,17 @@ cudaError_t ensure_smem_limit_fn(const void* kern, size_t bytes) {
     static std::mutex mu;
     static std::unordered_map<uint64_t, size_t> done;  // (device, kernel) -> limit set
     const uint64_t key = (reinterpret_cast<uint64_t>(kern) << 8) ^ (uint64_t)(dev & 0xFF);
-    {
-        std::lock_guard<std::mutex> g(mu);
-        auto it = done.find(key);
-        if (it != done.end() && it->second >= bytes) return cudaSuccess;
-    }
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-    if (e != cudaSuccess) return e;
+    // one caller at a time up to the attribute, so that none lowers a limit another has raised
     std::lock_guard<std::mutex> g(mu);
-    size_t& v = done[key];
-    if (bytes > v) v = bytes;
-    return cudaSuccess;
+    try {
+        size_t& v = done[key];
+        if (v >= bytes) return cudaSuccess;
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+        if (e == cudaSuccess) v = bytes;
+        return e;
+    } catch (...) {  // out of memory: no exception leaves a C entry
+        return cudaErrorMemoryAllocation;
+    }
 }
 
 namespace {

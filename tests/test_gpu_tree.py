@@ -588,3 +588,33 @@ def test_the_short_way_and_the_long_way_agree(rmm, monkeypatch):
     for g in got:
         for a, b in zip(g, want):
             assert torch.equal(a, b)
+
+
+def test_calls_from_several_threads(rmm):
+    """Each thread on its own stream, with rows that need different amounts of shared memory: the same bits as
+    one after the other."""
+    import threading
+
+    xs = [normal(n, 32, n).cuda() for n in (16384, 24576, 65536, 131072)]
+    want = [rmm.rmm_softmax(x, 0.9) for x in xs]
+    torch.cuda.synchronize()
+    got, wrong = [None] * len(xs), []
+
+    def work(i):
+        try:
+            s = torch.cuda.Stream()
+            y = torch.zeros_like(want[i])
+            s.wait_stream(torch.cuda.default_stream())
+            for _ in range(50):
+                rmm.rmm_softmax(xs[i], 0.9, Y=y, stream=s)
+            s.synchronize()
+            got[i] = y
+        except Exception as e:
+            wrong.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(xs))]
+    [t.start() for t in threads]
+    [t.join() for t in threads]
+    assert not wrong
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
