@@ -31,7 +31,7 @@
 //   warps 0-7  softmax: S from TMEM, mask, running maximum, P (bf16) over S's own
 //              columns, O rescaled only when the maximum grew by more than 2^8;
 //              the query operand at the start of a unit, its output at the end
-//   warps 8, 9 MMA, a thread for each group: S = Q_S K_S^T for the group's next step
+//   warps 8, 9 MMA, a warp for each group: S = Q_S K_S^T for the group's next step
 //              as soon as its P.V is done, P.V (A from TMEM) as soon as its P is written
 //   warp 10    key and value blocks by tile copies through two rings, running ahead
 //              over units
@@ -43,6 +43,13 @@
 // are zeroed in shared memory before P.V: 0 times what they hold could be NaN.
 // Every wait is bounded: on expiry the kernel records RMM_ERR_TIMEOUT, all roles
 // leave their loops, copies and MMAs in flight drain, TMEM is freed.
+//
+// Measured (whole calls): 32 sequences x 8k keys, one node, every dim 101 us, 5.8 TB/s
+// of the keys and values; 8 x 16k, 25 nodes, half of the dims 64 us (5.7 TB/s in the
+// main loop); 4 x 32k, 64 nodes of 8 heads per KV head, every dim 254 us, 1030
+// TFLOP/s, the tensor cores 53 % busy; 1 x 2k, 16 nodes 21 us, three kernels' latency.
+// Of a step of two groups the products take 1261 cycles alone, whatever the softmax
+// does beside them, and 2000 with it.
 #include <math.h>
 
 #include "rmm_common.cuh"

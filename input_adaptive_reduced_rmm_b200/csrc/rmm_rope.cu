@@ -20,10 +20,10 @@
 // all 8 belong to the call.
 //
 // Measured: 4096 tokens of 64 + 8 + 8 heads move their 168 MB (beside what stays in
-// L2) in 38.8 us, 4.3 TB/s counted on the data alone; 64 sequences of one token
-// take 7 us.  Steps at 4096 tokens: a whole warp per row 101 us, half-warps 57,
+// L2) in 37.7 us, 4.5 TB/s counted on the data alone; 64 sequences of one token
+// take 6.3 us.  Steps at 4096 tokens: a whole warp per row 101 us, half-warps 57,
 // quarter-warps with packed arithmetic 43, four rows in flight and 64 tokens per
-// CTA 38.8 (two rows 42, 32 tokens 41).
+// CTA 38 (two rows 42, 32 tokens 41).
 #include "rmm_common.cuh"
 #include "rmm_internal.h"
 #include "rmm_tree.cuh"
