@@ -106,7 +106,7 @@ struct TreeArgs {
 };
 
 __device__ __forceinline__ int blocks_of(const TreeArgs& a, int b) {
-    const int len = __ldcg(a.lens + b);
+    const int len = a.lens[b];
     return len < 0 || len > a.ldL - a.T ? 0 : (len + a.T + BK - 1) / BK;
 }
 
@@ -316,10 +316,10 @@ __global__ void __launch_bounds__(tree_threads(kAll), 1)
         tma_prefetch_desc(&vmap);
         tma_prefetch_desc(&qmap);
     }
-    // Lengths, trees, queries and caches come from kernels before this call.  Where the kept sets'
-    // kernel goes first, it has waited for those before it let this one start, and only what reads
-    // the sets waits for it; reads before that go past the L1 cache.
-    if (kAll) pdl_wait();
+    // Lengths, trees, queries and caches come from kernels before this call, the kept sets from the
+    // one before.  Nothing is read ahead of this wait: that the kept sets' kernel has waited for the
+    // others makes their writes visible to it, not to this grid.
+    pdl_wait();
     pdl_launch_dependents();
     if (warp == 0) {
         // the CTA's share of the whole cost, and where it starts; the last CTA also leaves the
@@ -332,7 +332,7 @@ __global__ void __launch_bounds__(tree_threads(kAll), 1)
             const int nb = b == lane ? mine : blocks_of(a, b);
             blocks += nb;
             seqs += nb > 0;
-            if (blockIdx.x == 0 && __ldcg(a.lens + b) > a.ldL - a.T) record_status(status, RMM_ERR_INVALID_ARG);
+            if (blockIdx.x == 0 && a.lens[b] > a.ldL - a.T) record_status(status, RMM_ERR_INVALID_ARG);
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) {
@@ -405,7 +405,7 @@ __global__ void __launch_bounds__(tree_threads(kAll), 1)
             const int rp = pair_of(a, w.u), plane = w.b * a.Hkv + head_of(a, w.u);
             const int tiles = 2 * rp + 1 < a.nrt ? 2 : 1;
             const size_t row0 = (size_t)plane * a.R;
-            if (a.parents && tid < a.T) par[tid] = __ldcg(a.parents + (size_t)w.b * a.T + tid);
+            if (a.parents && tid < a.T) par[tid] = a.parents[(size_t)w.b * a.T + tid];
             if (kAll) {
                 if (tid == 0) {
                     const uint32_t qf = smem_addr(&bars->q_full), qb = smem_addr(sQ);
@@ -426,10 +426,9 @@ __global__ void __launch_bounds__(tree_threads(kAll), 1)
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
                         const int r = (2 * rp + t) * BM + c16 * 8 + e;
-                        v[t][e] = t < tiles && r < a.R ? __ldcg(reinterpret_cast<const uint4*>(a.Q + (row0 + r) * D + c * 8))
+                        v[t][e] = t < tiles && r < a.R ? *reinterpret_cast<const uint4*>(a.Q + (row0 + r) * D + c * 8)
                                                        : make_uint4(0, 0, 0, 0);
                     }
-                pdl_wait();  // the kept sets
                 const int32_t* S = a.idx + (size_t)plane * a.k;
                 int d[4];
 #pragma unroll
@@ -479,7 +478,7 @@ __global__ void __launch_bounds__(tree_threads(kAll), 1)
             const int g = head_of(a, w.u), rp = pair_of(a, w.u);
             const bool two = 2 * rp + 1 < a.nrt;
             const int plane = w.b * a.Hkv + g;
-            const int len = __ldcg(a.lens + w.b);
+            const int len = a.lens[w.b];
             const int tile = 2 * rp + (two ? grp : 0);
             const int row = tile * BM + i;  // of the unit's G * T rows: query head row / T, node row % T
             const size_t row0 = (size_t)plane * a.R;
@@ -802,7 +801,6 @@ __global__ void __launch_bounds__(tree_threads(kAll), 1)
         // instruction takes about 110 cycles to leave, so that two warps of them bounded the
         // kernel (1750 cycles a block at 64 kept dims, where its bytes take 1000).
         const int c16 = lane & 7, row = (warp - kGatherWarp) * 4 + (lane >> 3);
-        pdl_wait();
         Ring k;
         bool ok = true;
         for (bool more = w.next(a, bars, true); ok && more; more = w.next(a, bars, false)) {
@@ -833,7 +831,6 @@ __global__ void __launch_bounds__(tree_threads(kAll), 1)
         cp_async_wait_all();  // no copy may still be landing when the CTA leaves
     }
 
-    if (!kAll) pdl_wait();  // nothing is left of the kept sets' kernel when this one ends
     tc_fence_before();
     __syncthreads();
     tc_fence_after();

@@ -38,6 +38,12 @@ constexpr int kRowThreads = 128, kRowCtas = 6, kRowFly = 4;
 constexpr int kEightParts = 65536;
 constexpr float kLog2e = 1.4426950408889634f;
 
+// The cluster's barrier wants whole warps: lanes that a condition has parted meet first.
+__device__ __forceinline__ void cluster_meet() {
+    __syncwarp();
+    cluster_sync();
+}
+
 __device__ __forceinline__ float ld_shared_cluster_f32(uint32_t addr) {
     float v;
     asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
@@ -147,7 +153,7 @@ __global__ void __launch_bounds__(kThreads)
         for (int w = 0; w < kThreads / 32; ++w) best = min(best, red_i[w]);
         if (nc > 1) {
             if (tid == 0) part[0] = m, part[1] = __int_as_float(best);
-            cluster_sync();
+            cluster_meet();
             float M = -INFINITY;
             for (int j = 0; j < nc; ++j) M = fmaxf(M, ld_shared_cluster_f32(mapa_shared(smem_addr(&part[0]), j)));
             best = 0x7FFFFFFF;
@@ -155,7 +161,7 @@ __global__ void __launch_bounds__(kThreads)
                 if (ld_shared_cluster_f32(mapa_shared(smem_addr(&part[0]), j)) == M)
                     best = min(best, __float_as_int(ld_shared_cluster_f32(mapa_shared(smem_addr(&part[1]), j))));
             m = M;
-            cluster_sync();
+            cluster_meet();
         }
         if (m == -INFINITY) best = -1;  // nothing but -inf: no probability anywhere
         float* y = Y + row * ldy;
@@ -184,12 +190,12 @@ __global__ void __launch_bounds__(kThreads)
     for (int w = 0; w < kThreads / 32; ++w) s += red_s[w];
     if (nc > 1) {
         if (tid == 0) part[0] = m, part[1] = s;
-        cluster_sync();
+        cluster_meet();
         m = -INFINITY, s = 0.f;
         for (int j = 0; j < nc; ++j)
             merge(m, s, ld_shared_cluster_f32(mapa_shared(smem_addr(&part[0]), j)),
                   ld_shared_cluster_f32(mapa_shared(smem_addr(&part[1]), j)), c);
-        cluster_sync();  // no CTA leaves while another still reads its pair
+        cluster_meet();  // no CTA leaves while another still reads its pair
     }
     const float inv = s == 0.0f ? 0.0f : 1.0f / s, ref_row = reference(m);
     float* y = Y + row * ldy;
@@ -292,7 +298,7 @@ __global__ void __launch_bounds__(kRowThreads, kRowCtas)
         merge(m, s, m2, s2, c);
     }
     if (tid == 0) part[0] = m, part[1] = s;
-    cluster_sync();
+    cluster_meet();
     m = -INFINITY, s = 0.f;
 #pragma unroll
     for (int j = 0; j < kParts; ++j)
@@ -317,7 +323,7 @@ __global__ void __launch_bounds__(kRowThreads, kRowCtas)
         const float v = __uint_as_float((uint32_t)X[row * ldx + vecs * 8 + tid] << 16);
         Y[row * ldy + vecs * 8 + tid] = ex2((v - ref) * c) * inv;
     }
-    cluster_sync();  // no CTA leaves while another still reads its pair
+    cluster_meet();  // no CTA leaves while another still reads its pair
 }
 
 template <int NV>

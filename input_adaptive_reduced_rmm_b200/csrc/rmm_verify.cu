@@ -42,6 +42,12 @@ constexpr int kCtas = 8;
 constexpr int kAll = kCtas * kWarps;  // warps of a sequence
 constexpr int kStep = 128;            // indices a warp takes at once, 4 per lane
 
+// The cluster's barrier wants whole warps: lanes that a condition has parted meet first.
+__device__ __forceinline__ void cluster_meet() {
+    __syncwarp();
+    cluster_sync();
+}
+
 __device__ __forceinline__ void st_shared_cluster_f64(uint32_t addr, double v) {
     asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(addr), "d"(v) : "memory");
 }
@@ -186,7 +192,7 @@ __global__ void __launch_bounds__(kThreads)
         uv[tid] = (double)u[node0 + tid];
     }
     if (tid == 0) way[0] = 0, w.mass[0] = 1.0;
-    cluster_sync();  // every CTA of the cluster runs, its shared memory can be written
+    cluster_meet();  // every CTA of the cluster runs, its shared memory can be written
     if (par[0] != -1) {  // an empty slot of the batch
         if (rank == 0) {
             if (tid < T) path[node0 + tid] = emitted[node0 + tid] = -1;
@@ -230,7 +236,7 @@ __global__ void __launch_bounds__(kThreads)
         acc = warp_sum(acc);
         double* const slot = part[passes & 1];  // the other one may still be read by a slower CTA
         if (lane < kCtas) st_shared_cluster_f64(mapa_shared(smem_addr(&slot[me]), lane), acc);
-        cluster_sync();
+        cluster_meet();
         double t = 0.0;
 #pragma unroll
         for (int i = 0; i < kAll / 32; ++i) t += slot[lane * (kAll / 32) + i];

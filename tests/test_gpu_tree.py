@@ -258,6 +258,32 @@ def test_attn_tree_captured_and_replayed_with_other_lengths(rmm):
     assert rmm.rmm_get_status(ws) == rmm.RMM_OK
 
 
+def test_attn_tree_many_calls_with_inputs_just_written(rmm):
+    """Lengths, trees, queries and caches written by the kernels directly before each call, into the buffers of
+    the call before, kept sets into a buffer of -1: every call sees its own."""
+    B, T, Hq, Hkv, ldL, k = 24, 4, 16, 4, 1024, 48
+    ws = rmm.new_workspace(rmm.rmm_attn_tree_workspace_bytes(B, Hq, Hkv, T, ldL))
+    g = torch.Generator(device="cuda").manual_seed(1)
+    Q, O = (torch.zeros(B, Hq, T, D, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    Kt, V = torch.zeros(B, Hkv, D, ldL, dtype=torch.bfloat16, device="cuda"), torch.zeros(B, Hkv, ldL, D, dtype=torch.bfloat16, device="cuda")
+    lens, idx = torch.zeros(B, dtype=torch.int32, device="cuda"), torch.zeros(B, Hkv, k, dtype=torch.int32, device="cuda")
+    Kt.normal_(generator=g)
+    for i in range(300):
+        Q.normal_(generator=g)
+        v = 1.0 + i % 7  # equal values: so is every output that has seen only this call's
+        V.fill_(v)
+        idx.fill_(-1)
+        lens.random_(-1, ldL - T + 1, generator=g)
+        rmm.rmm_attn_tree(Q, Kt, V, lens, k / D, O=O, idx_out=idx, workspace=ws)
+        s = Q.view(B, Hkv, -1, D).abs().amax(2)
+        want = torch.sort(torch.sort(s, dim=-1, descending=True, stable=True).indices[..., :k], -1).values.int()
+        there = lens >= 0
+        assert torch.equal(idx, torch.where(there[:, None, None], want, -1)), i
+        # a weighted mean of v with weights P / l, P rounded to bf16 (2^-8), then O rounded (2^-8)
+        want = torch.where(there, v, 0.0)[:, None, None, None]
+        assert bool(((O.float() - want).abs() <= 2.1 * H16 * v).all()), i
+
+
 def test_attn_tree_on_two_streams_with_their_own_workspaces(rmm):
     cases = [attn_inputs(2, 10, 8, 2, [700, 300], 1024, "padded", s, junk=False) for s in (21, 22)]
     want = [rmm.rmm_attn_tree(*cuda(*c[:4]), 0.5, parents=c[4].cuda()) for c in cases]
