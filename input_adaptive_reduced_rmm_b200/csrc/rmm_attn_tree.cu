@@ -44,10 +44,10 @@
 // Every wait is bounded: on expiry the kernel records RMM_ERR_TIMEOUT, all roles
 // leave their loops, copies and MMAs in flight drain, TMEM is freed.
 //
-// Measured (whole calls): 32 sequences x 8k keys, one node, every dim 101 us, 5.8 TB/s
-// of the keys and values; 8 x 16k, 25 nodes, half of the dims 64 us (5.7 TB/s in the
-// main loop); 4 x 32k, 64 nodes of 8 heads per KV head, every dim 254 us, 1030
-// TFLOP/s, the tensor cores 53 % busy; 1 x 2k, 16 nodes 21 us, three kernels' latency.
+// Measured (whole calls): 32 sequences x 8k keys, one node, every dim 102 us, 5.8 TB/s
+// of the keys and values; 8 x 16k, 25 nodes, half of the dims 68 us (5.7 TB/s in the
+// main loop); 4 x 32k, 64 nodes of 8 heads per KV head, every dim 260 us, 1000
+// TFLOP/s, the tensor cores 53 % busy; 1 x 2k, 16 nodes 22 us, three kernels' latency.
 // Of a step of two groups the products take 1261 cycles alone, whatever the softmax
 // does beside them, and 2000 with it.
 #include <math.h>

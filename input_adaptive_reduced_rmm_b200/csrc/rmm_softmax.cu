@@ -12,11 +12,15 @@
 //                        copied to shared memory at once and read there twice: six CTAs
 //                        per SM in different phases
 // Measured, us for (rows, V), registers against parts:
-//   (16, 32000) 5.1 4.2   (32, 16384) 4.2 4.3     (32, 131072) 10.4 10.1
-//   (64, 8192) 3.9 4.2    (64, 32000) 12.5 6.0    (512, 8192) 13.1 12.1
-//   (512, 16384) 25.9 16.0                        (512, 131072) 126 75
-// so parts are taken from 32 rows of 16384 logits on, where rows start on 16-byte
-// boundaries.  (512, 131072) moves its 403 MB at 5.4 TB/s; the two exponentials per
+//   (8, 16384) 3.2 3.3    (8, 131072) 6.2 6.3     (16, 16384) 3.3 3.3
+//   (16, 32000) 5.2 4.2   (16, 131072) 8.8 8.0    (64, 8192) 3.9 4.2
+//   (64, 32000) 12.5 6.0  (512, 16384) 25.9 16.0  (512, 131072) 126 75
+// and for rows that start at any element (registers one element at a time)
+//   (1, 2051) 2.2 2.4     (1, 4099) 4.5 2.7       (512, 2051) 7.3 9.5
+//   (1, 50257) 8.1 4.6    (512, 8195) 40 12       (512, 131069) 444 73
+// so parts are taken from 16 rows of 16384 logits on where rows start on 16-byte
+// boundaries, and above 4096 logits where they do not but logits and outputs start
+// alike, the up to 7 elements at either end one by one.  (512, 131072) moves its 403 MB at 5.4 TB/s; the two exponentials per
 // element take 35 us beside that.  Slower at 512 x 131072 were a second read from L2
 // instead of shared memory (80), two 16-byte stores instead of one of 32 (99) and a
 // wave of resident clusters over many rows (169).
@@ -33,7 +37,7 @@ constexpr int kThreads = 512;
 // softmax_rows_kernel: when it is taken, its threads, CTAs per SM and vectors of a thread
 // at a time, and the length from which a row has 8 parts instead of 4 (us, 4 against 8 parts:
 // 23.6 and 28.1 at 512 x 32000, 80.8 and 75.5 at 512 x 131072; 256 threads 28.5 and 79.8).
-constexpr int kManyRows = 32, kLongRow = 16384;
+constexpr int kManyRows = 16, kLongRow = 16384, kRaggedRow = 4097;
 constexpr int kRowThreads = 128, kRowCtas = 6, kRowFly = 4;
 constexpr int kEightParts = 65536;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -231,10 +235,15 @@ __global__ void __launch_bounds__(kRowThreads, kRowCtas)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int64_t row = blockIdx.x / kParts;
     const int rank = blockIdx.x % kParts;
-    const int vecs = V / 8, lo = rank * per, n = min(vecs - lo, per);  // this CTA's vectors
-    const bool tail = rank == kParts - 1 && vecs * 8 + tid < V;        // the last, partial vector
-    const uint16_t* x = X + row * ldx + (int64_t)lo * 8;
-    float* y = Y + row * ldy + (int64_t)lo * 8;
+    // elements before the row's first 16-byte boundary, whole vectors, elements after the last
+    const uint16_t* xr = X + row * ldx;
+    float* yr = Y + row * ldy;
+    const int head = (int)((16 - (reinterpret_cast<uintptr_t>(xr) & 15)) & 15) / 2;
+    const int vecs = (V - head) / 8, lo = rank * per, n = min(vecs - lo, per);  // this CTA's vectors
+    const int end = head + vecs * 8;
+    const int extra = rank == 0 && tid < head ? tid : rank == kParts - 1 && end + tid < V ? end + tid : -1;
+    const uint16_t* x = xr + head + (int64_t)lo * 8;
+    float* y = yr + head + (int64_t)lo * 8;
     const int group = (per + kGroups * kStep - 1) / (kGroups * kStep) * kStep;
     pdl_wait();
     pdl_launch_dependents();
@@ -280,8 +289,8 @@ __global__ void __launch_bounds__(kRowThreads, kRowCtas)
                 for (int e = 0; e < 8; ++e) s += ex2((at(r[i], e) - ref) * c);
         }
     }
-    if (tail) {
-        const float v = __uint_as_float((uint32_t)X[row * ldx + vecs * 8 + tid] << 16);
+    if (extra >= 0) {
+        const float v = __uint_as_float((uint32_t)xr[extra] << 16);
         merge(m, s, fmaxf(v, -INFINITY), ex2((v - reference(v)) * c), c);
     }
 #pragma unroll
@@ -319,9 +328,9 @@ __global__ void __launch_bounds__(kRowThreads, kRowCtas)
             store8(y + (int64_t)(i0 + i * kRowThreads) * 8, p, whole);
         }
     }
-    if (tail) {
-        const float v = __uint_as_float((uint32_t)X[row * ldx + vecs * 8 + tid] << 16);
-        Y[row * ldy + vecs * 8 + tid] = ex2((v - ref) * c) * inv;
+    if (extra >= 0) {
+        const float v = __uint_as_float((uint32_t)xr[extra] << 16);
+        yr[extra] = ex2((v - ref) * c) * inv;
     }
     cluster_meet();  // no CTA leaves while another still reads its pair
 }
@@ -351,11 +360,16 @@ cudaError_t launch(const uint16_t* X, int rows, int V, int64_t ldx, float temper
     return cudaLaunchKernelEx(&cfg, softmax_kernel<NV>, X, V, ldx, c, one_hot, Y, ldy, nc, wide, wide_y);
 }
 
+// Whether an element that starts 16 bytes of a row of X starts 32 bytes of the row of Y, in every row.
+bool alike(const uint16_t* X, int64_t ldx, const float* Y, int64_t ldy) {
+    return (reinterpret_cast<uintptr_t>(X) / 2 - reinterpret_cast<uintptr_t>(Y) / 4) % 8 == 0 && (ldx - ldy) % 8 == 0;
+}
+
 template <int kParts>
 cudaError_t launch_rows(const uint16_t* X, int rows, int V, int64_t ldx, float temperature, float* Y, int64_t ldy,
                         cudaStream_t stream) {
     const int per = (V / 8 / kParts + 32) & ~31;  // vectors of a part, the last one's fewer
-    const bool whole = (reinterpret_cast<uintptr_t>(Y) & 31) == 0 && ldy % 8 == 0;
+    const bool whole = alike(X, ldx, Y, ldy);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)rows * kParts);
     cfg.blockDim = dim3(kRowThreads);
@@ -382,7 +396,8 @@ cudaError_t launch_softmax(const uint16_t* X, int rows, int V, int64_t ldx, floa
     const int vecs = (V + 7) / 8;
     const bool aligned = (reinterpret_cast<uintptr_t>(X) & 15) == 0 && ldx % 8 == 0 &&
                          (reinterpret_cast<uintptr_t>(Y) & 15) == 0 && ldy % 4 == 0;
-    if (aligned && temperature != 0.0f && rows >= kManyRows && V >= kLongRow)
+    const bool ragged = !aligned && alike(X, ldx, Y, ldy);  // rows that start anywhere
+    if (temperature != 0.0f && ((aligned && rows >= kManyRows && V >= kLongRow) || (ragged && V >= kRaggedRow)))
         return V >= kEightParts ? launch_rows<8>(X, rows, V, ldx, temperature, Y, ldy, stream)
                                 : launch_rows<4>(X, rows, V, ldx, temperature, Y, ldy, stream);
     int nc = 1;

@@ -319,7 +319,10 @@ def test_softmax(rmm, rows, V, t):
 
 @pytest.mark.parametrize("rows,V,ldx,ldy", [(32, 16384, 16384, 16384), (33, 16391, 16392, 16396), (40, 20000, 20008, 20008),
                                             (32, 65543, 65544, 65544), (35, 131072, 131072, 131076),
-                                            (32, 262144, 262144, 262144)])
+                                            (32, 262144, 262144, 262144),
+                                            # rows that start anywhere, the outputs' like the logits' or not
+                                            (9, 2049, 2049, 2049), (17, 2051, 2051, 2059), (5, 50257, 50257, 50257),
+                                            (33, 65537, 65537, 65537), (3, 131069, 131069, 131069), (9, 4099, 4099, 4100)])
 def test_softmax_many_long_rows(rmm, rows, V, ldx, ldy):
     X = normal(V, rows, ldx, std=3.0)
     X[1, : V - 4] = -math.inf  # mass in the last part alone
