@@ -141,7 +141,8 @@ struct Share {
     }
 };
 
-// A place in a ring of stages: its slot and the parity of its round.
+// A place in a ring of stages: its slot and the parity of its round (attn_tree_rings says what
+// depths the parity allows).
 struct Ring {
     int slot = 0;
     uint32_t phase = 0;
@@ -1018,6 +1019,29 @@ size_t cum_bytes(int B) { return ((size_t)(B + 3) * sizeof(long long) + 255) / 2
 
 }  // namespace
 
+// Two stages each, then more values and keys by turns while they fit.
+// A wait for a full barrier tells a round of its slot by parity, so it also passes two rounds
+// early, while the copy of the round before is still on its way.  Whoever waits for a block
+// therefore has to know that the one before it in its slot has landed.  A group that takes every
+// block waits for that one itself; with one row tile (the last of an odd number) it takes every
+// second block, and only an even depth brings it back to the slots it has waited for.  (A wait
+// for the blocks between would not do: their slots may have been filled again by then.)  The
+// softmax warps, which wait for values only near a sequence's end, know that the products of
+// the block two before in their group are done: four stages with one row tile, which every
+// size gives.  At a piece's start all blocks of the pieces before have been used.
+TreeRings attn_tree_rings(int nrt, int kp) {
+    const int kb = kp * 128, by = nrt % 2 ? 2 : 1;
+    const int fixed = 1024 + (nrt > 1 ? 2 : 1) * kp * 256 + (int)sizeof(TreeBars) + kTreeMax * 4;
+    TreeRings r{2, 2, 0};
+    for (bool grew = true; grew;) {
+        grew = false;
+        if (r.nv < kMaxStages && fixed + (r.nv + by) * V_BYTES + r.nk * kb <= kSmemMax) r.nv += by, grew = true;
+        if (r.nk < kMaxStages && r.nk < r.nv && fixed + r.nv * V_BYTES + (r.nk + by) * kb <= kSmemMax) r.nk += by, grew = true;
+    }
+    r.smem = fixed + r.nv * V_BYTES + r.nk * kb;
+    return r;
+}
+
 size_t attn_tree_partial_bytes(int B, int Hq, int Hkv, int T, int ldL, int num_sms) {
     const TreePlan p = tree_plan(B, Hq, Hkv, T, ldL, num_sms);
     return cum_bytes(B) + (size_t)p.ctas * 2 * slot_floats(p.slot_rows) * sizeof(float);
@@ -1049,16 +1073,9 @@ cudaError_t launch_attn_tree(const CUtensorMap& qmap, const CUtensorMap& kmap, c
     a.k = k;
     a.kp = (k + 15) / 16 * 16;
     a.scale_log2 = scale * 1.4426950408889634f;
-    // rings: two stages each, then more values and keys by turns while they fit
-    const int kb = a.kp * 128;
-    const int fixed = 1024 + (p.nrt > 1 ? 2 : 1) * a.kp * 256 + (int)sizeof(TreeBars) + kTreeMax * 4;
-    a.nk = a.nv = 2;
-    for (bool grew = true; grew;) {
-        grew = false;
-        if (a.nv < kMaxStages && fixed + (a.nv + 1) * V_BYTES + a.nk * kb <= kSmemMax) ++a.nv, grew = true;
-        if (a.nk < kMaxStages && a.nk < a.nv && fixed + a.nv * V_BYTES + (a.nk + 1) * kb <= kSmemMax) ++a.nk, grew = true;
-    }
-    const size_t smem = fixed + (size_t)a.nv * V_BYTES + (size_t)a.nk * kb;
+    const TreeRings rings = attn_tree_rings(p.nrt, a.kp);
+    a.nk = rings.nk, a.nv = rings.nv;
+    const size_t smem = rings.smem;
     auto* kern = a.identity ? attn_tree_kernel<true> : attn_tree_kernel<false>;
     cudaError_t e = ensure_smem_limit(kern, smem);
     if (e != cudaSuccess) return e;

@@ -192,6 +192,12 @@ cudaError_t launch_qkv_rope(const uint16_t* Yq, const uint16_t* Yk, const uint16
                             const uint16_t* q_norm, const uint16_t* k_norm, float eps, const float* inv_freq, int rot,
                             int interleaved, const int32_t* lens, int L0, const int32_t* parents, uint16_t* Q,
                             uint16_t* Kt, uint16_t* V, int ldL, int num_sms, cudaStream_t stream);
+// Stages of its key and value rings for units of nrt 128-row tiles and kp (a multiple of 16) kept dims, and the
+// shared memory they come to.
+struct TreeRings {
+    int nk, nv, smem;
+};
+TreeRings attn_tree_rings(int nrt, int kp);
 // Bytes of split partials for these sizes.
 size_t attn_tree_partial_bytes(int B, int Hq, int Hkv, int T, int ldL, int num_sms);
 // qmap: Q as rows of 128 dims, box 64 x 128; kmap: Kt as [plane][dim][key], box 64 keys x 128
