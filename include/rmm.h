@@ -391,8 +391,10 @@ size_t rmm_attn_tree_workspace_bytes(int B, int Hq, int Hkv, int T, int ldL, int
  *   O[b,q,t,:] = softmax_l(logit) . V[b,g,l,:]   (full d, fp32 softmax).
  * Absent nodes and empty slots get O = 0 (their kept set entries in idx_out are
  * left as they were for empty slots).  Key and value slots that no node sees
- * may hold anything.  With T = 1 and parents NULL this is plain decoding of a
- * batch of different lengths.
+ * may hold anything.  A NaN or +inf logit makes its row NaN, a row of nothing but
+ * -inf logits is 0; a NaN or infinite value at a slot of the cache or of a present
+ * node reaches every node of its sequence (its weight is 0 where it is not seen).
+ * With T = 1 and parents NULL this is plain decoding of a batch of different lengths.
  *   Q, O bf16 [B, Hq, T, d]; Kt bf16 [B, Hkv, d, ldL]; V bf16 [B, Hkv, ldL, d]
  *   idx_out int32 [B, Hkv, k] or NULL
  * A length without room (lens[b] > ldL - T) is reported through

@@ -41,6 +41,8 @@
 // caches lay them out, Q K-major (a tile copy) or, gathered, MN-major.  TMEM
 // holds S0, S1, O0, O1 (128 columns each).  Value rows past a sequence's slots
 // are zeroed in shared memory before P.V: 0 times what they hold could be NaN.
+// A row that sees no key has the sum 0 and the output 0; a NaN sum (a NaN or +inf logit)
+// is the row's answer, in whatever piece it arose.
 // Every wait is bounded: on expiry the kernel records RMM_ERR_TIMEOUT, all roles
 // leave their loops, copies and MMAs in flight drain, TMEM is freed.
 //
@@ -594,7 +596,7 @@ __global__ void __launch_bounds__(tree_threads(kAll), 1)
             more = w.next(a, bars, false);
             if (more) open();
             if (two) {
-                const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+                const float inv = 1.0f / l;
                 const int sr = grp * BM + i;
                 if (!whole && row < a.R) {
                     slot[D * a.slot_rows + sr] = m_use;
@@ -613,7 +615,7 @@ __global__ void __launch_bounds__(tree_threads(kAll), 1)
                         for (int v = 0; v < 4; ++v) {
                             float f[8];
 #pragma unroll
-                            for (int e = 0; e < 8; ++e) f[e] = l > 0.0f ? __uint_as_float(o[v * 8 + e]) * inv : 0.0f;
+                            for (int e = 0; e < 8; ++e) f[e] = l == 0.0f ? 0.0f : __uint_as_float(o[v * 8 + e]) * inv;
                             dst[v] = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]),
                                                 pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
                         }
@@ -629,7 +631,7 @@ __global__ void __launch_bounds__(tree_threads(kAll), 1)
                 const float M = fmaxf(m0, m1);
                 const float w0 = m0 == -INFINITY ? 0.0f : exp2f(m0 - M), w1 = m1 == -INFINITY ? 0.0f : exp2f(m1 - M);
                 const float L = w0 * l0 + w1 * l1;
-                const float inv = whole ? (L > 0.0f ? 1.0f / L : 0.0f) : 1.0f;
+                const float inv = whole ? (L == 0.0f ? 0.0f : 1.0f / L) : 1.0f;
                 if (!whole && row < a.R && grp == 0) {
                     slot[D * a.slot_rows + i] = M;
                     slot[(D + 1) * a.slot_rows + i] = L;
@@ -866,7 +868,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_tree_join_kernel(const Tree
     const int skip = nb && total * c0 / C < p0 ? 1 : 0;
     const float* base = a.partials + (size_t)(2 * (c0 * a.side + (a.side > 1 ? rp : 0))) * sf;
     const size_t at = ((size_t)c4 * a.slot_rows + row) * 4;
-    float M = -INFINITY, L = 0.f;
+    float M = -INFINITY, L = 0.f, nan = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int i0 = z; i0 < n; i0 += kFly * kLanes) {
         float m[kFly], l[kFly];
@@ -874,7 +876,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_tree_join_kernel(const Tree
 #pragma unroll
         for (int i = 0; i < kFly; ++i) {
             const int j = i0 + i * kLanes;
-            m[i] = -INFINITY;
+            m[i] = -INFINITY, l[i] = 0.f;
             if (j < n) {
                 const float* p = base + (size_t)(2 * j * a.side + (j == 0 ? skip : 0)) * sf;
                 m[i] = p[D * a.slot_rows + row];
@@ -884,7 +886,10 @@ __global__ void __launch_bounds__(kJoinThreads) attn_tree_join_kernel(const Tree
         }
         float top = M;
 #pragma unroll
-        for (int i = 0; i < kFly; ++i) top = fmaxf(top, m[i]);
+        for (int i = 0; i < kFly; ++i) {
+            top = fmaxf(top, m[i]);
+            if (isnan(l[i])) nan = l[i];  // the row's, whatever its piece weighs
+        }
         if (top == -INFINITY) continue;  // the row has seen no key
         const float keep = exp2f(M - top);
         M = top;
@@ -902,6 +907,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_tree_join_kernel(const Tree
             }
         }
     }
+    L += nan;
 #pragma unroll
     for (int d = 1; d < kLanes; d *= 2) {
         const float top = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
@@ -916,7 +922,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_tree_join_kernel(const Tree
         o.w += __shfl_xor_sync(0xffffffffu, o.w, d);
     }
     if (z > 0 || r >= rows) return;
-    const float inv = L > 0.f ? 1.0f / L : 0.f;
+    const float inv = L == 0.f ? 0.f : 1.0f / L;
     *reinterpret_cast<uint2*>(a.O + (((size_t)b * a.Hkv + g) * a.R + rp * 2 * BM + r) * D + c4 * 4) =
         make_uint2(pack2(o.x * inv, o.y * inv), pack2(o.z * inv, o.w * inv));
 }

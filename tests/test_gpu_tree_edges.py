@@ -4,7 +4,8 @@ Tolerances as in test_gpu_tree.py."""
 import pytest
 import torch
 
-from test_gpu_tree import D, attn_inputs, check_attn, cuda, rmm  # noqa: F401 (a fixture)
+import tree_ref as ref
+from test_gpu_tree import D, H16, H32, attn_inputs, check_attn, cuda, rmm  # noqa: F401 (a fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -45,3 +46,60 @@ def test_attn_tree_repeats_its_bits(rmm, B, T, Hq, Hkv, lens, ldL, r):  # noqa: 
         wrong += (O != want).sum()
     assert int(wrong) == 0
     assert rmm.rmm_get_status(ws) == rmm.RMM_OK
+
+
+BAD = [  # B, T, Hq, Hkv, lens, ldL: whole units and cut ones, of one row tile and of two
+    (90, 1, 8, 2, [3 + i for i in range(90)], 96),
+    (90, 20, 8, 2, [3 + i for i in range(90)], 120),
+    (1, 16, 8, 2, [5000], 5016),
+    (90, 33, 8, 2, [3 + i for i in range(90)], 128),
+    (2, 64, 16, 2, [900, 61], 968),
+]
+
+
+@pytest.mark.parametrize("B,T,Hq,Hkv,lens,ldL", BAD)
+@pytest.mark.parametrize("where,value,r", [("query", "nan", 1.0), ("query row", "nan", 1.0), ("query row", "inf", 1.0),
+                                           ("key", "nan", 1.0), ("key", "nan", 0.5), ("key", "inf", 0.5),
+                                           ("node's key", "nan", 1.0), ("value", "nan", 0.5), ("value", "inf", 1.0)])
+def test_attn_tree_nan_stays_nan(rmm, B, T, Hq, Hkv, lens, ldL, where, value, r):  # noqa: F811
+    """NaN and infinite queries, keys and values reach exactly the outputs that the formula gives them
+    (a query's its own row, a key's the rows that see it), however the work is cut."""
+    Q, Kt, V, lens, parents = attn_inputs(B, T, Hq, Hkv, lens, ldL, "full", 40, junk=False)
+    bad, G, t = float(value), Hq // Hkv, T // 2
+    for b in range(0, B, 2):
+        n = int(lens[b])
+        if where == "query":
+            Q[b, 1, t, 5] = bad
+        elif where == "query row":
+            Q[b, G, t] = bad
+        elif where == "key":
+            Kt[b, 1, :, n // 2] = bad
+        elif where == "node's key":
+            Kt[b, 0, :, n + t] = bad
+        else:
+            V[b, 1, n // 2, 7] = bad
+    wo, wi, A, X = ref.attn_tree(Q, Kt, V, lens, parents, r)
+    q, kt, v, ln, pr = cuda(Q, Kt, V, lens, parents)
+    idx = torch.full((B, Hkv, rmm.rmm_k_for(D, r)), -1, dtype=torch.int32, device="cuda")
+    O = rmm.rmm_attn_tree(q, kt, v, ln, r, parents=pr, idx_out=idx).double().cpu()
+    if where not in ("query", "query row"):
+        assert torch.equal(idx.cpu(), wi)
+    assert bool(torch.isnan(wo).any()) or value == "inf"
+    assert torch.equal(torch.isnan(O), torch.isnan(wo))
+    assert torch.equal(torch.isinf(O), torch.isinf(wo))
+    fine = torch.isfinite(wo)
+    tol = H16 * wo.abs() + (H16 + 2e-4 + 2 * (idx.shape[-1] + 2) * H32 * X[..., None]) * A
+    assert bool(((O - wo).abs() <= tol)[fine].all())
+
+
+@pytest.mark.parametrize("B,T,Hq,Hkv,lens,ldL", BAD)
+def test_attn_tree_rows_of_minus_infinity(rmm, B, T, Hq, Hkv, lens, ldL):  # noqa: F811
+    """Nothing but -inf logits: 0, beside a head whose rows are as ever."""
+    Q, Kt, V, lens, parents = attn_inputs(B, T, Hq, Hkv, lens, ldL, "full", 41, junk=False)
+    Q = Q.abs() + 0.125
+    Kt[:, 0] = -float("inf")
+    O = rmm.rmm_attn_tree(*cuda(Q, Kt, V, lens), 1.0, parents=parents.cuda()).cpu()
+    G = Hq // Hkv
+    assert not bool(O[:, :G].any())
+    wo, _, A, X = ref.attn_tree(Q[:, G:], Kt[:, 1:], V[:, 1:], lens, parents, 1.0)
+    assert bool(((O[:, G:].double() - wo).abs() <= H16 * wo.abs() + (H16 + 2e-4 + 260 * H32 * X[..., None]) * A).all())
