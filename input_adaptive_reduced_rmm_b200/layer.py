@@ -229,16 +229,22 @@ class OutputHead:
         return rmm.rmm_softmax(logits, temperature)
 
 
+def _common_pos(layers) -> int:
+    """How many tokens every layer's cache holds."""
+    if any(layer.pos != layers[0].pos for layer in layers):
+        raise ValueError("the layers' caches hold different numbers of tokens")
+    return layers[0].pos
+
+
 def keep_path(layers, path: torch.Tensor, count: torch.Tensor, lens: torch.Tensor | None = None) -> int:
     """Keep the nodes path[0, :count[0]] (int32 [1, T], ascending) of the tree that forward_tree scored last, in
     every layer's cache: their keys and values move up to the cache, pos grows by their number, which is returned
     (it is read from the device)."""
-    if any(layer.pos != layers[0].pos for layer in layers):
-        raise ValueError("the layers' caches hold different numbers of tokens")
+    pos = _common_pos(layers)
     if lens is None:
-        lens = torch.full((1,), layers[0].pos, dtype=torch.int32, device=path.device)
+        lens = torch.full((1,), pos, dtype=torch.int32, device=path.device)
     grown = rmm.rmm_cache_keep([(layer.Kt.unsqueeze(0), layer.V.unsqueeze(0)) for layer in layers], lens, path, count)
-    n = int(grown) - layers[0].pos
+    n = int(grown) - pos
     for layer in layers:
         layer.pos += n
     return n
@@ -253,8 +259,9 @@ def decode_tree(layers, head: OutputHead, embed: torch.Tensor, tokens: torch.Ten
     children were drawn from (None: certain picks).  Returns the tokens emitted, one more than the drafts that were
     accepted: the last of them is the next tree's root.  For any draft they are distributed as sampling one token
     at a time from the layers would have them, given the kept sets of this pass."""
+    pos = _common_pos(layers)  # before the first layer writes its nodes there
     tokens, parents, u = tokens.view(1, -1), parents.view(1, -1), u.view(1, -1)
-    lens = torch.full((1,), layers[0].pos, dtype=torch.int32, device=tokens.device)
+    lens = torch.full((1,), pos, dtype=torch.int32, device=tokens.device)
     x = embed.index_select(0, tokens[0].clamp(0, embed.shape[0] - 1))  # other tokens are never accepted
     for layer in layers:
         x = layer.forward_tree(x, parents, lens)
