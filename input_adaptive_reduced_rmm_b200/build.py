@@ -28,7 +28,7 @@ BINDING = os.path.join(PKG, "_binding.so")
 
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
-CFLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC]
+CFLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Werror", "all-warnings", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC]
 
 
 def _deps():

@@ -120,7 +120,8 @@ __device__ __forceinline__ int pair_of(const TreeArgs& a, int u) { return a.side
 // costs nb + piece: the places [0, piece) stand for the start and end of its pieces, place
 // piece + i for block i.
 struct Share {
-    int b, u, x, left, cost, blk, n, nb;  // blk, n: the piece's first block and how many, nb: of the whole unit
+    // blk, n: the piece's first block and how many, nb: of the whole unit
+    int b = 0, u = 0, x = 0, left = 0, cost = 0, blk = 0, n = 0, nb = 0;
     __device__ __forceinline__ bool next(const TreeArgs& a, const TreeBars* s, bool first) {
         if (first) {
             b = s->seg_b, u = s->seg_u, x = s->seg_x, left = s->cost;
