@@ -25,6 +25,7 @@ OBJ = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "librmm.so")
 BINDING_SRC = os.path.join(CSRC, "binding.cpp")
 BINDING = os.path.join(PKG, "_binding.so")
+BINDING_FOR = os.path.join(OBJ, "_binding.for")  # what it was compiled against
 
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -56,9 +57,27 @@ def _compile(src, verbose_ptxas):
     return obj, p.stderr
 
 
+def _binding_target():
+    """The torch and Python that the module uses the C++ and C interfaces of: it fits no others."""
+    import torch
+
+    return f"torch {torch.__version__} {torch.version.git_version} {torch.compiled_with_cxx11_abi()}, " \
+           f"python {sys.implementation.cache_tag} {sys.hexversion:#x}\n"
+
+
+def _binding_stale():
+    if _stale(BINDING, [BINDING_SRC, os.path.join(INCLUDE, "rmm.h")]):
+        return True
+    try:
+        with open(BINDING_FOR) as f:
+            return f.read() != _binding_target()
+    except OSError:
+        return True
+
+
 def _build_binding(force):
     """Compile csrc/binding.cpp into _binding.so, which finds librmm.so beside itself."""
-    if not force and not _stale(BINDING, [BINDING_SRC, os.path.join(INCLUDE, "rmm.h")]):
+    if not force and not _binding_stale():
         return
     import torch
     from torch.utils import cpp_extension
@@ -74,6 +93,9 @@ def _build_binding(force):
     if p.returncode != 0:
         raise RuntimeError(f"g++ failed for {BINDING_SRC}:\n{p.stdout}\n{p.stderr}")
     os.replace(tmp, BINDING)
+    with open(BINDING_FOR + f".tmp{os.getpid()}", "w") as f:
+        f.write(_binding_target())
+    os.replace(BINDING_FOR + f".tmp{os.getpid()}", BINDING_FOR)
 
 
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:
