@@ -449,7 +449,7 @@ rmm_status rmm_tree_verify(const float* P, int64_t ldp, const float* Qd, int64_t
  * pointers; different caches, one per layer), the key and value at slot
  * lens[b] + path[b,i] move to slot lens[b] + i for i < kept[b], and
  * lens_out[b] = lens[b] + kept[b] (lens_out NULL: not written; it may be lens
- * itself, and must not overlap it otherwise).
+ * itself, and must not overlap it otherwise, nor path or kept).
  *   Kts[c] bf16 [B, Hkv, d, ldL], Vs[c] bf16 [B, Hkv, ldL, d], in place
  *   path   int32 [B, T], ascending within the first kept[b] entries, in [0, T)
  * A sequence with kept[b] outside [1, T], an empty slot or a path that is not

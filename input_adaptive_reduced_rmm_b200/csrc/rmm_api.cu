@@ -814,8 +814,10 @@ rmm_status rmm_cache_keep(int count, void* const* Kts, void* const* Vs, int B, i
         return RMM_ERR_INVALID_ARG;
     if (d != 128 || T > kTreeMax || count > kMaxCaches || B > kTreeMaxBatch || Hkv > kTreeMaxHeads)
         return RMM_ERR_UNSUPPORTED;
-    // lens_out is lens itself, or apart from it
-    if (lens_out && lens_out != lens && lens_out < lens + B && lens < lens_out + B) return RMM_ERR_INVALID_ARG;
+    // lens_out is lens itself, or apart from it, and apart from what the CTAs read beside it
+    auto over = [&](const int32_t* p, size_t n) { return lens_out < p + n && p < lens_out + B; };
+    if (lens_out && ((lens_out != lens && over(lens, B)) || over(kept, B) || over(path, (size_t)B * T)))
+        return RMM_ERR_INVALID_ARG;
     CacheList c;
     for (int i = 0; i < count; ++i) {
         if (!Kts[i] || !Vs[i] || !aligned16(Kts[i]) || !aligned16(Vs[i])) return RMM_ERR_INVALID_ARG;
