@@ -446,7 +446,7 @@ rmm_status rmm_tree_verify(const float* P, int64_t ldp, const float* Qd, int64_t
                            int32_t* emitted, int32_t* count, rmm_stream_t stream);
 
 /* The accepted nodes kept: in each of `count` caches (host arrays of device
- * pointers; different caches, one per layer), the key and value at slot
+ * pointers; caches that do not overlap, one per layer), the key and value at slot
  * lens[b] + path[b,i] move to slot lens[b] + i for i < kept[b], and
  * lens_out[b] = lens[b] + kept[b] (lens_out NULL: not written; it may be lens
  * itself, and must not overlap it otherwise, nor path or kept).

@@ -4,6 +4,7 @@
 #include <math.h>
 #include <string.h>
 
+#include <algorithm>
 #include <mutex>
 #include <unordered_map>
 
@@ -819,13 +820,19 @@ rmm_status rmm_cache_keep(int count, void* const* Kts, void* const* Vs, int B, i
     if (lens_out && ((lens_out != lens && over(lens, B)) || over(kept, B) || over(path, (size_t)B * T)))
         return RMM_ERR_INVALID_ARG;
     CacheList c;
+    uintptr_t at[2 * kMaxCaches];
     for (int i = 0; i < count; ++i) {
         if (!Kts[i] || !Vs[i] || !aligned16(Kts[i]) || !aligned16(Vs[i])) return RMM_ERR_INVALID_ARG;
-        for (int j = 0; j < i; ++j)  // one cache twice would be moved twice
-            if (Kts[i] == Kts[j] || Vs[i] == Vs[j]) return RMM_ERR_INVALID_ARG;
         c.Kt[i] = static_cast<uint16_t*>(Kts[i]);
         c.V[i] = static_cast<uint16_t*>(Vs[i]);
+        at[2 * i] = reinterpret_cast<uintptr_t>(Kts[i]);
+        at[2 * i + 1] = reinterpret_cast<uintptr_t>(Vs[i]);
     }
+    // caches that overlap (one twice, say) would be moved twice
+    std::sort(at, at + 2 * count);
+    const uint64_t bytes = (uint64_t)B * Hkv * d * ldL * sizeof(uint16_t);
+    for (int i = 1; i < 2 * count; ++i)
+        if (at[i] - at[i - 1] < bytes) return RMM_ERR_INVALID_ARG;
     return cuda_status(launch_cache_keep(c, count, B, Hkv, ldL, lens, path, kept, T, lens_out,
                                          static_cast<cudaStream_t>(stream)));
 }
