@@ -701,10 +701,11 @@ def _rows(t, name, dtype, rows=None, V=None):
 
 def _node_rows(t, name, B, T, V):
     """A row per node, [B, T, V] contiguous or [B*T, V] with a row stride: the stride."""
-    if t.dtype == torch.float32 and t.is_contiguous() and t.shape == (B, T, V):
-        return V
-    if t.dim() == 3 and t.is_contiguous():
+    if t.dim() == 3 and t.is_contiguous() and 1 in t.shape[:2]:  # rows in a row, without a batch of their own
         t = t.flatten(0, 1)
+    elif t.dim() == 3:
+        _need(t, name, torch.float32, shape=(B, T, V))
+        return V
     return _rows(t, name, torch.float32, B * T, V)
 
 
