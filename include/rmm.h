@@ -67,9 +67,9 @@ typedef struct rmm_options {
     int attn_per_query_head;
     /* Split count of the decode GEMV; 0 = automatic. */
     int gemv_splits;
-    /* Watchdog self-test: nonzero makes the reduced GEMM wait, with a 50 ms
-     * limit, on a barrier that nothing signals; the call then reports
-     * RMM_ERR_TIMEOUT through rmm_get_status() and leaves Y unspecified. */
+    /* Watchdog self-test: nonzero makes the reduced GEMM and rmm_attn_tree wait,
+     * with a 50 ms limit, on a barrier that nothing signals; the call then reports
+     * RMM_ERR_TIMEOUT through rmm_get_status() and leaves Y (O) unspecified. */
     int debug_timeout_test;
     /* Operand producer of the reduced GEMM: 0 (default) = the CTA-pair
      * kernel, sixteen warps per CTA gathering the kept rows with 16-byte

@@ -783,7 +783,8 @@ rmm_status rmm_attn_tree(const void* Q, const void* Kt, const void* V, const int
                                         Hq, Hkv, T, ldL, k, scale, lens, parents, static_cast<uint16_t*>(O),
                                         idx_out ? idx_out : reinterpret_cast<int32_t*>(ws + kStatusBytes),
                                         idx_out != nullptr, ws + kStatusBytes + idx_bytes, reinterpret_cast<int*>(ws),
-                                        sms, static_cast<cudaStream_t>(stream)));
+                                        opts_or_default(options).debug_timeout_test, sms,
+                                        static_cast<cudaStream_t>(stream)));
 }
 
 rmm_status rmm_softmax(const void* X, int rows, int V, int64_t ldx, float temperature, float* Y, int64_t ldy,

@@ -88,6 +88,7 @@ struct __align__(8) TreeBars {
     uint64_t s_full[2][2], p_full[2][2];  // [group][buffer]
     uint64_t pv_done[2];
     uint64_t meet;  // all softmax warps
+    uint64_t never;  // watchdog self-test: nothing ever arrives here
     int seg_b, seg_u, seg_x, cost, piece;  // the CTA's share: where it starts, and how much it is
     uint32_t tmem_base;
     int abort_flag;
@@ -104,6 +105,7 @@ struct TreeArgs {
     int B, Hkv, G, T, ldL, R, nrt, nrp, k, kp, nk, nv, slot_rows;
     int side, U;  // row pairs that CTAs of their own take side by side (or 1), units of a sequence then
     int identity;    // every dim kept
+    int debug_timeout;
     float scale_log2;
 };
 
@@ -308,6 +310,7 @@ __global__ void __launch_bounds__(tree_threads(kAll), 1)
             mbar_init(smem_addr(&bars->pv_done[s]), 1);
         }
         mbar_init(smem_addr(&bars->meet), 8);
+        mbar_init(smem_addr(&bars->never), 1);
         bars->abort_flag = 0;
         fence_mbar_init();
     }
@@ -736,6 +739,9 @@ __global__ void __launch_bounds__(tree_threads(kAll), 1)
             uint32_t pv = 0;          // P.V products issued: block pv of the group is in buffer pv & 1
             int piece = 0;
             bool ok = true;
+            // the self-test's wait runs out after the debug limit, and every role leaves
+            if (a.debug_timeout && g == 0)
+                ok = __all_sync(0xffffffffu, mbar_wait(smem_addr(&bars->never), 0, status, abort_flag, kDebugWaitLimitNs));
             for (bool more = w.next(a, bars, true); ok && more; more = w.next(a, bars, false), ++piece) {
                 // with two row tiles every block is this group's, with one every second
                 const bool two = 2 * pair_of(a, w.u) + 1 < a.nrt;
@@ -1057,7 +1063,7 @@ size_t attn_tree_partial_bytes(int B, int Hq, int Hkv, int T, int ldL, int num_s
 cudaError_t launch_attn_tree(const CUtensorMap& qmap, const CUtensorMap& kmap, const CUtensorMap& vmap,
                              const uint16_t* Q, const uint16_t* Kt, int B, int Hq, int Hkv, int T, int ldL, int k, float scale,
                              const int32_t* lens, const int32_t* parents, uint16_t* O, int32_t* idx, int want_idx,
-                             void* partials, int* status, int num_sms, cudaStream_t stream) {
+                             void* partials, int* status, int debug_timeout, int num_sms, cudaStream_t stream) {
     const TreePlan p = tree_plan(B, Hq, Hkv, T, ldL, num_sms);
     TreeArgs a{};
     a.Q = Q;
@@ -1070,6 +1076,7 @@ cudaError_t launch_attn_tree(const CUtensorMap& qmap, const CUtensorMap& kmap, c
     a.cum = static_cast<long long*>(partials);
     a.partials = reinterpret_cast<float*>(static_cast<uint8_t*>(partials) + cum_bytes(B));
     a.status = status;
+    a.debug_timeout = debug_timeout;
     a.B = B, a.Hkv = Hkv, a.G = Hq / Hkv, a.T = T, a.ldL = ldL;
     a.R = p.R, a.nrt = p.nrt, a.nrp = p.nrp, a.slot_rows = p.slot_rows;
     // Row pairs of a head that CTAs take side by side read its keys and values at the same time, so

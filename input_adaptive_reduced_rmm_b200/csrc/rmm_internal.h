@@ -206,7 +206,8 @@ size_t attn_tree_partial_bytes(int B, int Hq, int Hkv, int T, int ldL, int num_s
 cudaError_t launch_attn_tree(const CUtensorMap& qmap, const CUtensorMap& kmap, const CUtensorMap& vmap,
                              const uint16_t* Q, const uint16_t* Kt, int B, int Hq, int Hkv, int T, int ldL, int k,
                              float scale, const int32_t* lens, const int32_t* parents, uint16_t* O, int32_t* idx,
-                             int want_idx, void* partials, int* status, int num_sms, cudaStream_t stream);
+                             int want_idx, void* partials, int* status, int debug_timeout, int num_sms,
+                             cudaStream_t stream);
 constexpr int kSoftmaxMaxV = 262144;  // logits per row
 cudaError_t launch_softmax(const uint16_t* X, int rows, int V, int64_t ldx, float temperature, float* Y, int64_t ldy,
                            cudaStream_t stream);

@@ -103,3 +103,20 @@ def test_attn_tree_rows_of_minus_infinity(rmm, B, T, Hq, Hkv, lens, ldL):  # noq
     assert not bool(O[:, :G].any())
     wo, _, A, X = ref.attn_tree(Q[:, G:], Kt[:, 1:], V[:, 1:], lens, parents, 1.0)
     assert bool(((O[:, G:].double() - wo).abs() <= H16 * wo.abs() + (H16 + 2e-4 + 260 * H32 * X[..., None]) * A).all())
+
+
+@pytest.mark.parametrize("B,T,Hq,Hkv,lens,ldL,r", [(3, 5, 8, 2, [700, 30, -1], 1024, 1.0), (3, 5, 8, 2, [700, 30, -1], 1024, 0.5),
+                                                   (2, 64, 16, 2, [900, 61], 968, 1.0), (2, 64, 16, 2, [900, 61], 968, 0.5),
+                                                   (1, 40, 8, 1, [2000], 2040, 0.75)])
+def test_attn_tree_watchdog(rmm, B, T, Hq, Hkv, lens, ldL, r):  # noqa: F811
+    """A wait that runs out (50 ms) is reported, the call ends, and the next one on the same workspace is as ever."""
+    Q, Kt, V, lens, parents = attn_inputs(B, T, Hq, Hkv, lens, ldL, "padded", 43, junk=False)
+    args, pr = cuda(Q, Kt, V, lens), parents.cuda()
+    want = rmm.rmm_attn_tree(*args, r, parents=pr)
+    ws = rmm.new_workspace(rmm.rmm_attn_tree_workspace_bytes(B, Hq, Hkv, T, ldL))
+    for _ in range(2):
+        rmm.rmm_attn_tree(*args, r, parents=pr, workspace=ws, opts=rmm.options(debug_timeout_test=True))
+        assert rmm.rmm_get_status(ws) == rmm.RMM_ERR_TIMEOUT
+        got = rmm.rmm_attn_tree(*args, r, parents=pr, workspace=ws)
+        assert rmm.rmm_get_status(ws) == rmm.RMM_OK
+        assert torch.equal(got, want)
