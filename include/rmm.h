@@ -352,7 +352,8 @@ rmm_status rmm_heads_to_tokens(const void* O, int Hq, int T, int d, void* A, rmm
  *            parents[b,t] in [0, t), or is a root (-1); any other value marks it
  *            absent (padding), and a node below an absent one is absent.
  *            NULL, where allowed: a chain, node t hangs on node t - 1.
- * B <= 4096, at most 4096 heads of a kind (RMM_ERR_UNSUPPORTED above). */
+ * B <= 4096, at most 4096 heads of a kind (RMM_ERR_UNSUPPORTED above).  Where a call
+ * does not say otherwise its outputs overlap neither its inputs nor each other. */
 
 /* The q/k/v projections of B sequences of T tokens (token-major, as
  * rmm_linear_group writes them) into the attention layouts, with per-head RMS

@@ -46,10 +46,14 @@
 // Every wait is bounded: on expiry the kernel records RMM_ERR_TIMEOUT, all roles
 // leave their loops, copies and MMAs in flight drain, TMEM is freed.
 //
-// Measured (whole calls): 32 sequences x 8k keys, one node, every dim 102 us, 5.8 TB/s
-// of the keys and values; 8 x 16k, 25 nodes, half of the dims 68 us (5.7 TB/s in the
-// main loop); 4 x 32k, 64 nodes of 8 heads per KV head, every dim 260 us, 1000
-// TFLOP/s, the tensor cores 53 % busy; 1 x 2k, 16 nodes 22 us, three kernels' latency.
+// Measured (whole calls in long rows, on changing inputs): 32 sequences x 8k keys, one
+// node, every dim 115 us, 5.1 TB/s of the keys and values (104 and 5.7 in a row of 60);
+// 8 x 16k, 25 nodes, half of the dims 70 us (5.7 TB/s in the main loop); 4 x 32k, 64
+// nodes of 8 heads per KV head, every dim 311 us, 845 TFLOP/s, the tensor cores 50 %
+// busy and the clock at 1.5 GHz; 1 x 2k, 16 nodes 22 us, three kernels' latency.
+// Fewer dims save bytes of K^T but bring the selection and the gather: 25 nodes at a
+// quarter, a half, three quarters, all of the dims 64, 69, 74, 68 us, one node of
+// 32 x 8k 103, 102, 102, 104.
 // Of a step of two groups the products take 1261 cycles alone, whatever the softmax
 // does beside them, and 2000 with it.
 #include <math.h>
@@ -204,8 +208,10 @@ __device__ __forceinline__ F2 add2_here(F2 a, F2 b) {
     return r;
 }
 
-// p = 2^(x scale - m) for 64 logits of a row, their sum, and P (bf16) to the 32
-// columns at pcol; kBatch exponentials are on their way while those before are summed.
+// p = 2^(x scale - m) for 64 logits of a row, their sum in 32 bits, and P to the 32
+// columns at pcol, rounded to bf16, V's type, since a product's operands have one type
+// (against 64 bits the outputs are off by 0.0023 of their norm, with P in 32 bits by
+// 0.0017, which is their own rounding).  kBatch exponentials are on their way while those before are summed.
 __device__ __forceinline__ float exp_block(uint32_t (&x)[2][32], float scale_log2, float neg_m, uint32_t pcol) {
     constexpr int kBatch = 16;
     F2 sum[4] = {F2(0.f, 0.f), F2(0.f, 0.f), F2(0.f, 0.f), F2(0.f, 0.f)};

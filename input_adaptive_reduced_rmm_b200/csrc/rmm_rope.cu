@@ -6,9 +6,11 @@
 //   (x'_i, x'_j) -> (x'_i c - x'_j s, x'_j c + x'_i s)     c + is = e^(i pos f_i)
 // for the rot/2 pairs (i, j) = (i, i + rot/2), or (2i, 2i+1) when interleaved.
 // Everything between the bf16 input and the one rounding to bf16 is fp32.  The
-// angle is a fraction of a turn in 64-bit fixed point: pos * round(2^64 f / 2 pi)
-// modulo 2^64, off by less than 2^-33 of a turn at any position (an fp32 angle
-// is off by 0.004 rad at position 10^5), its sine and cosine are fp32.
+// angle is a fraction of a turn in 64-bit fixed point, pos * round(2^64 f / 2 pi)
+// modulo 2^64, reduced to half a turn either way before it becomes fp32: off by at
+// most 2^-26 of a turn from that rounding, 2^-32 from the bits below it and
+// pos f 2^-54 from the frequency's product in fp64 (an angle formed in fp32 is off
+// by 0.004 rad at position 10^5).  Sine and cosine are fp32.
 //
 // Memory bound: each element is read once and written once.  A quarter-warp holds
 // one (token, head) row of 128 dims; a lane has 8 dims and the 8 that they are
@@ -20,8 +22,9 @@
 // all 8 belong to the call.
 //
 // Measured: 4096 tokens of 64 + 8 + 8 heads move their 168 MB (beside what stays in
-// L2) in 37.7 us, 4.5 TB/s counted on the data alone; 64 sequences of one token
-// take 6.3 us.  Steps at 4096 tokens: a whole warp per row 101 us, half-warps 57,
+// L2) in 39 us, 4.3 TB/s counted on the data alone; 64 sequences of one token
+// take 6.5 us, trees of 25 nodes of 8 sequences 9.3, of 64 nodes of 16 sequences
+// (32 + 8 + 8 heads) 17.8.  Steps at 4096 tokens: a whole warp per row 101 us, half-warps 57,
 // quarter-warps with packed arithmetic 43, four rows in flight and 64 tokens per
 // CTA 38 (two rows 42, 32 tokens 41).
 #include "rmm_common.cuh"
@@ -37,8 +40,9 @@ constexpr int kRopeThreads = 256;
 constexpr int kFly = 4;  // heads' rows in flight
 // Tokens per CTA; heads per CTA of q and v (the angles of a token serve them all) and of k
 // (each with its shared tile).  A batch of single tokens that would have more CTAs than
-// places (two per SM) takes more heads per CTA: 64 sequences, 64 + 8 + 8 heads, 256 CTAs
-// instead of 576, 6.3 us instead of 7.0; 8 sequences, which fit, 4.4 instead of 3.8.
+// places (two per SM) takes more heads per CTA: 64 sequences of 32 + 8 + 8 heads 192 CTAs
+// instead of 448, 6.5 us instead of 7.3, of 64 + 8 + 8 heads 256 instead of 576, 6.5 instead of
+// 7.7; 8 sequences, which fit, 4.5 instead of 3.9.
 struct RopeTile {
     int tokens, heads, key_heads;
 };

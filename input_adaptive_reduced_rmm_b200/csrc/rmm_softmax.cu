@@ -20,7 +20,11 @@
 //   (1, 50257) 8.1 4.6    (512, 8195) 40 12       (512, 131069) 444 73
 // so parts are taken from 16 rows of 16384 logits on where rows start on 16-byte
 // boundaries, and above 4096 logits where they do not but logits and outputs start
-// alike, the up to 7 elements at either end one by one.  (512, 131072) moves its 403 MB at 5.4 TB/s; the two exponentials per
+// alike, the up to 7 elements at either end one by one.  Temperature 0, and logits and
+// outputs that start unlike, keep to the registers with one store per element, which
+// long rows feel: (512, 131072) at temperature 0 402 us, (512, 131069) out of 131072
+// columns 395, (1, 32000) at temperature 0 5.4.
+// (512, 131072) moves its 403 MB at 5.2 TB/s; the two exponentials per
 // element take 35 us beside that.  Slower at 512 x 131072 were a second read from L2
 // instead of shared memory (80), two 16-byte stores instead of one of 32 (99) and a
 // wave of resident clusters over many rows (169).

@@ -18,14 +18,15 @@
 // of the vocabulary.  The tests need one probability each, fetched up front for all
 // nodes; the rows themselves are read only at a node where a child is rejected, and
 // at the last node, once: R (fp64) and the draft's row then stay in registers for
-// the node's further rejections and the search of the next token.  A vocabulary
-// above 131072 does not fit there; its passes read the rows again and repeat the
-// rejections so far.  A pass sends every warp's sum to all 8 CTAs, so one barrier of
+// the node's further rejections and the search of the next token (above 65536 tokens,
+// at eight steps a warp, 128 registers do not hold all of both: the compiler keeps 360
+// bytes of a thread's in local memory).  A vocabulary above 131072 does not fit there;
+// its passes read the rows again and repeat the rejections so far.  A pass sends every warp's sum to all 8 CTAs, so one barrier of
 // the cluster gives each of them the total and, for the next token, the place.
 // Latency bound: a node's rows take one exposed read, a rejection one barrier of the
-// cluster.  16 trees of 32 nodes over 131072 tokens take 28 us (57 us when every
-// pass read its rows again and the search walked 32 indices at a time), one chain of
-// 8 over 32000 tokens 8 us (18 us).
+// cluster.  16 trees of 32 nodes over 131072 tokens take 25 us, with certain picks 21
+// (57 us when every pass read its rows again and the search walked 32 indices at a
+// time), one chain of 8 over 32000 tokens 5.6 us (18 us).
 #include <math.h>
 
 #include "rmm_common.cuh"

@@ -208,7 +208,7 @@ class DecoderLayer:
 
 class OutputHead:
     """Hidden rows to next-token probabilities: RMSNorm, the product with the output weights [V, H] at ratio r,
-    softmax at a temperature."""
+    softmax at a temperature.  The rows between are kept per row count, so one head serves one stream at a time."""
 
     def __init__(self, weight: torch.Tensor, r: float, device, eps: float = 1e-5):
         self.Wt = rmm.rmm_transpose_weight(weight.to(device))
